@@ -32,6 +32,9 @@ ENTRY_POINTS = (
     "qlora_fwd_w16_workspace_bytes", "qlora_bwd_w16_workspace_bytes", "qlora_linear_fwd_w16",
     "qlora_linear_bwd_w16", "nf4_quantize_batch_workspace_bytes", "nf4_quantize_batch",
     "qlora_bwd_batch_workspace_bytes", "qlora_linear_bwd_batch", "nf4_dequantize_batch",
+    "qlora_act8_scales", "qlora_act8_quantize", "qlora_act8_dequantize", "qlora_act8_grad_a_workspace_bytes",
+    "qlora_act8_grad_a", "qlora_bwd_act8_workspace_bytes", "qlora_linear_bwd_act8", "qlora_rms_norm_fwd",
+    "qlora_rms_norm_bwd_workspace_bytes", "qlora_rms_norm_bwd", "qlora_lm_loss_workspace_bytes", "qlora_lm_loss",
 )
 
 
@@ -72,6 +75,11 @@ class _DequantItem(ctypes.Structure):
     _fields_ = [("w", ctypes.POINTER(_Nf4Tensor)), ("y", ctypes.c_void_p)]
 
 
+class _Act8(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
+
+
 _LIB = None
 
 
@@ -89,7 +97,7 @@ def load() -> ctypes.CDLL:
         raise RuntimeError(f"libqlora_nf4.so is not built ({path}); run bit_nf4_quantized_gb300.build")
     lib = ctypes.CDLL(path)
     i64, i32, sz, vp, f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
-    tp = ctypes.POINTER(_Nf4Tensor)
+    tp, ap = ctypes.POINTER(_Nf4Tensor), ctypes.POINTER(_Act8)
     sig = {
         "nf4_abi_version": (i32, []),
         "nf4_status_str": (ctypes.c_char_p, [i32]),
@@ -120,6 +128,19 @@ def load() -> ctypes.CDLL:
                                        vp, vp, vp, vp, sz, vp]),
         "qlora_bwd_batch_workspace_bytes": (sz, [i64, i32, ctypes.POINTER(_BwdItem), i32]),
         "qlora_linear_bwd_batch": (i32, [i64, i32, ctypes.POINTER(_BwdItem), i32, vp, sz, vp]),
+        "qlora_act8_scales": (i64, [i64, i64]),
+        "qlora_act8_quantize": (i32, [vp, i32, ap, vp]),
+        "qlora_act8_dequantize": (i32, [ap, vp, vp, i32, vp]),
+        "qlora_act8_grad_a_workspace_bytes": (sz, [i64, i64, i32]),
+        "qlora_act8_grad_a": (i32, [i32, f32, i32, vp, ap, vp, vp, vp, sz, vp]),
+        "qlora_bwd_act8_workspace_bytes": (sz, [i64, i64, i64, i32, i32, i32]),
+        "qlora_linear_bwd_act8": (i32, [i64, i64, i64, i32, f32, i32, i32, vp, ap, vp, vp, tp, vp, vp, vp,
+                                        vp, vp, vp, vp, sz, vp]),
+        "qlora_rms_norm_fwd": (i32, [i64, i64, f32, i32, vp, vp, vp, vp, vp, vp, ap, vp]),
+        "qlora_rms_norm_bwd_workspace_bytes": (sz, [i64, i64]),
+        "qlora_rms_norm_bwd": (i32, [i64, i64, i32, vp, vp, ap, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "qlora_lm_loss_workspace_bytes": (sz, [i64, i64, i64, i32, i32]),
+        "qlora_lm_loss": (i32, [i64, i64, i64, i32, vp, tp, vp, vp, i64, vp, i32, vp, vp, vp, vp, sz, vp]),
         "qlora_last_device_status": (i32, [vp, i32]),
         "nf4_kernel_launch_count": (i64, []),
         "qlora_debug_wait_timeout": (None, [i32]),
@@ -538,6 +559,286 @@ def qlora_bwd_batch_workspace_bytes(M: int, shapes, rank: int, dtype=torch.bfloa
         arr[i] = _BwdItem(N, K, rank, 1.0, SCALE_LORA, None, 16 if w16 else None, None, None, None, xid[i], None,
                           None, None, None)
     return int(lib.qlora_bwd_batch_workspace_bytes(M, len(shapes), arr, _dtype_code(dtype)))
+
+
+# ---- around the linear: the norm, 8-bit activation checkpoints, the loss ----------------------
+
+ACT8_BLOCK = 128
+
+
+class _Call:
+    """The tensors of one call: checked, made contiguous where the call only reads them, and
+    kept from reuse while the stream may still work on them."""
+
+    def __init__(self, name, device, stream):
+        if device.type != "cuda":
+            raise ValueError(f"{name}: CUDA tensors expected, got {device}")
+        self.name, self.device = name, device
+        current = torch.cuda.current_stream(device)
+        self.stream = current if stream is None else stream
+        self.elsewhere = self.stream != current
+
+    def _check(self, what, t, shape, dtype):
+        if not isinstance(t, torch.Tensor) or t.device != self.device:
+            raise ValueError(f"{self.name}: {what} must be a tensor on {self.device}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{self.name}: {what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.dtype != dtype:
+            raise ValueError(f"{self.name}: {what} is {t.dtype}, expected {dtype}")
+
+    def _used(self, t):
+        if self.elsewhere:
+            t.record_stream(self.stream)
+        return t
+
+    def read(self, what, t, shape, dtype):
+        """An input; a strided or misaligned one is copied (on the call's stream)."""
+        self._check(what, t, shape, dtype)
+        self._used(t)
+        if not t.is_contiguous() or t.data_ptr() % 16:
+            with torch.cuda.stream(self.stream):
+                t = t.clone(memory_format=torch.contiguous_format)
+        return t
+
+    def written(self, what, t, shape, dtype):
+        """An output: the caller's (contiguous) or a new one."""
+        if t is None:
+            return self._used(torch.empty(shape, dtype=dtype, device=self.device))
+        self._check(what, t, shape, dtype)
+        if not t.is_contiguous():
+            raise ValueError(f"{self.name}: {what} must be contiguous")
+        return self._used(t)
+
+    def stored(self, W):
+        """The C struct of an Nf4Tensor input."""
+        for t in (W.packed, W.absmax, W.nested_absmax, W.offset):
+            if t is not None:
+                self._used(t)
+        return W.c_struct()
+
+    def workspace(self, given, need):
+        ws = given if given is not None else _workspace(need, self.device)
+        return self._used(ws)
+
+    def run(self, fn, *args):
+        with torch.cuda.device(self.device):
+            _check(fn(*args, ctypes.c_void_p(self.stream.cuda_stream)), self.name)
+
+
+@dataclass
+class Act8:
+    """An activation [M, K] kept in 8 bits: int8 codes [M, K] and one float32 scale for each row
+    and block of 128 columns, [M, ceil(K / 128)]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @property
+    def shape(self) -> tuple:
+        return tuple(self.codes.shape)
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.scales.numel()
+
+    @staticmethod
+    def empty(M: int, K: int, device="cuda"):
+        return Act8(torch.empty((M, K), dtype=torch.int8, device=device),
+                    torch.empty((M, -(-K // ACT8_BLOCK)), dtype=torch.float32, device=device))
+
+
+def _act8_struct(call, c: Act8, M: int, K: int, write: bool):
+    """(C struct, tensors to keep) of a checkpoint of the given size."""
+    if not isinstance(c, Act8):
+        raise ValueError(f"{call.name}: an Act8 expected")
+    take = call.written if write else call.read
+    codes = take("codes", c.codes, (M, K), torch.int8)
+    scales = take("scales", c.scales, (M, -(-K // ACT8_BLOCK)), torch.float32)
+    return _Act8(M, K, codes.data_ptr(), scales.data_ptr()), (codes, scales)
+
+
+def _matrix(name, t, what="x"):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name}: {what} must be a 2-D tensor")
+    return t.shape
+
+
+def qlora_act8_quantize(x: torch.Tensor, out: Act8 = None, stream=None) -> Act8:
+    """x [M, K] (float32, bf16 or half) stored as int8 codes with one scale per 128 columns."""
+    lib = load()
+    M, K = _matrix("qlora_act8_quantize", x)
+    call = _Call("qlora_act8_quantize", x.device, stream)
+    x = call.read("x", x, (M, K), x.dtype)
+    out = Act8.empty(M, K, x.device) if out is None else out
+    cs, _keep = _act8_struct(call, out, M, K, True)
+    call.run(lib.qlora_act8_quantize, _ptr(x), _dtype_code(x.dtype), ctypes.byref(cs))
+    return out
+
+
+def qlora_act8_dequantize(c: Act8, dtype=torch.bfloat16, weight: torch.Tensor = None, out: torch.Tensor = None,
+                          stream=None) -> torch.Tensor:
+    """The values a checkpoint stands for (times weight [K] where given), [M, K] in dtype."""
+    lib = load()
+    M, K = c.shape
+    call = _Call("qlora_act8_dequantize", c.codes.device, stream)
+    cs, _keep = _act8_struct(call, c, M, K, False)
+    weight = None if weight is None else call.read("weight", weight, (K,), torch.float32)
+    y = call.written("out", out, (M, K), dtype if out is None else out.dtype)
+    call.run(lib.qlora_act8_dequantize, ctypes.byref(cs), _ptr(weight), _ptr(y), _dtype_code(y.dtype))
+    return y
+
+
+def qlora_act8_grad_a(G: torch.Tensor, c: Act8, alpha: float, mode: int = SCALE_LORA, weight: torch.Tensor = None,
+                      dA: torch.Tensor = None, workspace: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """dA = s G^T x [r, K] of an adapter whose input x is a checkpoint (times weight [K] where
+    given); G = dY B is float32 [M, r]."""
+    lib = load()
+    M, K = c.shape
+    r = _matrix("qlora_act8_grad_a", G, "G")[1]
+    call = _Call("qlora_act8_grad_a", G.device, stream)
+    G = call.read("G", G, (M, r), torch.float32)
+    cs, _keep = _act8_struct(call, c, M, K, False)
+    weight = None if weight is None else call.read("weight", weight, (K,), torch.float32)
+    dA = call.written("dA", dA, (r, K), torch.float32)
+    ws = call.workspace(workspace, 0 if workspace is not None else lib.qlora_act8_grad_a_workspace_bytes(M, K, r))
+    call.run(lib.qlora_act8_grad_a, r, ctypes.c_float(alpha), mode, _ptr(G), ctypes.byref(cs), _ptr(weight), _ptr(dA),
+             _ptr(ws), ws.numel())
+    return dA
+
+
+def qlora_linear_bwd_act8(dy: torch.Tensor, c: Act8, T: torch.Tensor, W, A: torch.Tensor, B: torch.Tensor,
+                          alpha: float, mode: int = SCALE_LORA, weight: torch.Tensor = None, dx: torch.Tensor = None,
+                          dA: torch.Tensor = None, dB: torch.Tensor = None, workspace: torch.Tensor = None,
+                          stream=None):
+    """qlora_linear_bwd with the input x kept as a checkpoint (times weight [K], the norm's,
+    where the checkpoint holds the normalised rows).  W is an Nf4Tensor, or the decoded weight
+    [N, K] in dy's dtype.  Returns (dX, dA, dB)."""
+    lib = load()
+    name = "qlora_linear_bwd_act8"
+    M, N = _matrix(name, dy, "dy")
+    r, K = _matrix(name, A, "A")
+    call = _Call(name, dy.device, stream)
+    dy = call.read("dy", dy, (M, N), dy.dtype)
+    cs, _keep = _act8_struct(call, c, M, K, False)
+    weight = None if weight is None else call.read("weight", weight, (K,), torch.float32)
+    T = call.read("T", T, (M, r), torch.float32)
+    A = call.read("A", A, (r, K), torch.float32)
+    B = call.read("B", B, (N, r), torch.float32)
+    stored = isinstance(W, Nf4Tensor)
+    if stored and tuple(W.shape) != (N, K):
+        raise ValueError(f"{name}: W has shape {tuple(W.shape)}, expected {(N, K)}")
+    w16 = None if stored else call.read("W", W, (N, K), dy.dtype)
+    wcs = call.stored(W) if stored else None
+    dx = call.written("dx", dx, (M, K), dy.dtype)
+    dA = call.written("dA", dA, (r, K), torch.float32)
+    dB = call.written("dB", dB, (N, r), torch.float32)
+    cd = _dtype_code(dy.dtype)
+    ws = call.workspace(workspace, 0 if workspace is not None else
+                        lib.qlora_bwd_act8_workspace_bytes(M, N, K, r, cd, int(not stored)))
+    call.run(lib.qlora_linear_bwd_act8, M, N, K, r, ctypes.c_float(alpha), mode, cd, _ptr(dy), ctypes.byref(cs),
+             _ptr(weight), _ptr(T), ctypes.byref(wcs) if stored else None, _ptr(w16), _ptr(A), _ptr(B), _ptr(dx),
+             _ptr(dA), _ptr(dB), _ptr(ws), ws.numel())
+    return dx, dA, dB
+
+
+def qlora_rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor = None,
+                       checkpoint=None, y: torch.Tensor = None, h: torch.Tensor = None, rstd: torch.Tensor = None,
+                       stream=None):
+    """h = x + residual, y = h / rms(h) * weight; returns (y, h, rstd, checkpoint).
+
+    x, residual [M, K]; weight [K] float32.  Without a residual h is x itself.  ``checkpoint``:
+    True or an Act8 stores the normalised rows h / rms(h), before the weight, in 8 bits."""
+    lib = load()
+    name = "qlora_rms_norm_fwd"
+    M, K = _matrix(name, x)
+    call = _Call(name, x.device, stream)
+    dt = x.dtype
+    given = x
+    x = call.read("x", x, (M, K), dt)
+    residual = None if residual is None else call.read("residual", residual, (M, K), dt)
+    weight = call.read("weight", weight, (K,), torch.float32)
+    y = call.written("y", y, (M, K), dt)
+    rstd = call.written("rstd", rstd, (M,), torch.float32)
+    stored = residual is not None or h is not None
+    h = call.written("h", h, (M, K), dt) if stored else given
+    cs = None
+    if checkpoint is True:
+        checkpoint = Act8.empty(M, K, x.device)
+    elif checkpoint is False:
+        checkpoint = None
+    if checkpoint is not None:
+        cs, _keep = _act8_struct(call, checkpoint, M, K, True)
+    call.run(lib.qlora_rms_norm_fwd, M, K, ctypes.c_float(eps), _dtype_code(dt), _ptr(x), _ptr(residual), _ptr(weight),
+             _ptr(y), _ptr(h) if stored else None, _ptr(rstd), None if cs is None else ctypes.byref(cs))
+    return y, h, rstd, checkpoint
+
+
+def qlora_rms_norm_bwd(dy: torch.Tensor, saved, rstd: torch.Tensor, weight: torch.Tensor,
+                       dresidual: torch.Tensor = None, dweight=None, dx: torch.Tensor = None,
+                       workspace: torch.Tensor = None, stream=None):
+    """Returns (dx, dweight) of qlora_rms_norm_fwd.  ``saved``: the forward's h or its checkpoint
+    (an Act8); ``dresidual``: the gradient that reaches h by the residual path; ``dweight``:
+    True or a float32 [K] tensor computes the weight's gradient."""
+    lib = load()
+    name = "qlora_rms_norm_bwd"
+    M, K = _matrix(name, dy, "dy")
+    call = _Call(name, dy.device, stream)
+    dt = dy.dtype
+    dy = call.read("dy", dy, (M, K), dt)
+    cs = h = None
+    if isinstance(saved, Act8):
+        cs, _keep = _act8_struct(call, saved, M, K, False)
+    else:
+        h = call.read("h", saved, (M, K), dt)
+    rstd = call.read("rstd", rstd, (M,), torch.float32)
+    weight = call.read("weight", weight, (K,), torch.float32)
+    dresidual = None if dresidual is None else call.read("dresidual", dresidual, (M, K), dt)
+    dx = call.written("dx", dx, (M, K), dt)
+    ws = None
+    if dweight is None or dweight is False:
+        dweight = None
+    else:
+        dweight = call.written("dweight", None if dweight is True else dweight, (K,), torch.float32)
+        ws = call.workspace(workspace, 0 if workspace is not None else lib.qlora_rms_norm_bwd_workspace_bytes(M, K))
+    call.run(lib.qlora_rms_norm_bwd, M, K, _dtype_code(dt), _ptr(dy), _ptr(h), None if cs is None else ctypes.byref(cs),
+             _ptr(rstd), _ptr(weight), _ptr(dresidual), _ptr(dx), _ptr(dweight), _ptr(ws),
+             0 if ws is None else ws.numel())
+    return dx, dweight
+
+
+def qlora_lm_loss(x: torch.Tensor, W, targets: torch.Tensor, grad_scale: torch.Tensor = None, ignore_index: int = -100,
+                  need_dx: bool = True, loss: torch.Tensor = None, lse: torch.Tensor = None, dx: torch.Tensor = None,
+                  workspace: torch.Tensor = None, stream=None):
+    """Softmax cross entropy of the frozen head W over its vocabulary; returns (loss, lse, dx).
+
+    x [M, D] bf16 or half; W [V, D] in x's dtype, or an Nf4Tensor; targets [M] int64, where
+    ``ignore_index`` marks a token that does not count (loss, lse and dx are zero).
+    ``grad_scale``: float32 [M] or [1], what dx is multiplied with (None: 1).  loss and lse are
+    float32 [M]; dx is None with need_dx=False.  A target outside the vocabulary sets the device
+    status word and counts as ignored."""
+    lib = load()
+    name = "qlora_lm_loss"
+    M, D = _matrix(name, x)
+    call = _Call(name, x.device, stream)
+    x = call.read("x", x, (M, D), x.dtype)
+    stored = isinstance(W, Nf4Tensor)
+    V = (W.shape if stored else _matrix(name, W, "W"))[0]
+    if stored and tuple(W.shape) != (V, D):
+        raise ValueError(f"{name}: W has shape {tuple(W.shape)}, expected {(V, D)}")
+    w16 = None if stored else call.read("W", W, (V, D), x.dtype)
+    wcs = call.stored(W) if stored else None
+    targets = call.read("targets", targets, (M,), torch.int64)
+    per_row = 0
+    if grad_scale is not None:
+        per_row = int(grad_scale.numel() != 1)
+        grad_scale = call.read("grad_scale", grad_scale.reshape(-1), (M if per_row else 1,), torch.float32)
+    loss = call.written("loss", loss, (M,), torch.float32)
+    lse = call.written("lse", lse, (M,), torch.float32)
+    dx = call.written("dx", dx, (M, D), x.dtype) if need_dx else None
+    ws = call.workspace(workspace, 0 if workspace is not None else
+                        lib.qlora_lm_loss_workspace_bytes(M, V, D, int(stored), int(need_dx)))
+    call.run(lib.qlora_lm_loss, M, V, D, _dtype_code(x.dtype), _ptr(x), ctypes.byref(wcs) if stored else None,
+             _ptr(w16), _ptr(targets), ignore_index, _ptr(grad_scale), per_row, _ptr(loss), _ptr(lse), _ptr(dx),
+             _ptr(ws), ws.numel())
+    return loss, lse, dx
 
 
 def debug_wait_timeout(on: bool = True):

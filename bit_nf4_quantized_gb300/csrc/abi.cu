@@ -16,6 +16,7 @@
 
 #include "common.cuh"
 #include "linear_tc.cuh"
+#include "train_ops.cuh"
 
 namespace qnf4 {
 
@@ -484,6 +485,12 @@ TcBwdItem tc_bwd_item(int64_t M, const qlora_bwd_item& it, float s, bool view = 
 }
 
 }  // namespace
+
+namespace qnf4 {
+nf4_status device_status_word(int** out) { return device_status_ptr(out); }
+nf4_status check_nf4_tensor(const nf4_tensor* t, int64_t numel) { return check_tensor(t, numel); }
+Nf4View nf4_view(const nf4_tensor* t) { return view_of(t); }
+}  // namespace qnf4
 
 extern "C" {
 
@@ -1022,6 +1029,71 @@ nf4_status qlora_linear_bwd_batch(int64_t M, int32_t count, const qlora_bwd_item
     if (e != cudaSuccess) return NF4_ERR_CUDA;
   }
   return NF4_OK;
+}
+
+namespace {
+// G fp32 [M, rank], the dA pass's partial sums, then the tensor-core path's workspace.
+struct Act8BwdWs {
+  size_t part, tc, total;
+  Act8BwdWs(int64_t M, int64_t N, int64_t K, int32_t rank, nf4_dtype cd, bool w16) {
+    part = a256(sizeof(float) * static_cast<size_t>(M) * rank);
+    tc = part + a256(act8_grad_ws_bytes(M, K, rank));
+    total = tc + (is16(cd) && M > 0 ? tc_bwd_ws_bytes(M, N, K, rank, w16) : 0);
+  }
+};
+}  // namespace
+
+size_t qlora_bwd_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t rank, nf4_dtype compute, int32_t w16) {
+  if (M < 0 || N <= 0 || K <= 0 || rank < 1 || rank > 256) return 0;
+  return Act8BwdWs(M, N, K, rank, compute, w16 != 0).total;
+}
+
+nf4_status qlora_linear_bwd_act8(int64_t M, int64_t N, int64_t K, int32_t rank, float alpha, qlora_scale_mode mode,
+                                 nf4_dtype compute, const void* dy, const qlora_act8* x, const float* x_weight,
+                                 const float* T, const nf4_tensor* W, const void* w16, const float* A, const float* B,
+                                 void* dx, float* dA, float* dB, void* ws, size_t ws_bytes, void* stream) {
+  float s = 0.0f;
+  nf4_status st = check_linear(M, N, K, rank, alpha, mode, compute, &s);
+  if (st != NF4_OK) return st;
+  if (w16 != nullptr) {
+    if (!is16(compute)) return NF4_ERR_DTYPE;
+    if (!aligned16(w16)) return NF4_ERR_ALIGN;
+  } else if ((st = check_tensor(W, N * K)) != NF4_OK) {
+    return st;
+  }
+  if (x == nullptr || A == nullptr || B == nullptr || dA == nullptr || dB == nullptr) return NF4_ERR_ARG;
+  if (x->rows != M || x->cols != K) return NF4_ERR_SHAPE;
+  if (M > 0 && (dy == nullptr || x->codes == nullptr || x->scales == nullptr || T == nullptr || dx == nullptr))
+    return NF4_ERR_ARG;
+  if (!aligned16(A) || !aligned16(B) || !aligned16(dA) || !aligned16(dB) || !aligned16(x_weight)) return NF4_ERR_ALIGN;
+  if (M > 0 && (!aligned16(dy) || !aligned16(x->codes) || !aligned16(x->scales) || !aligned16(T) || !aligned16(dx)))
+    return NF4_ERR_ALIGN;
+  const Act8BwdWs L(M, N, K, rank, compute, w16 != nullptr);
+  if (M > 0 && (ws == nullptr || ws_bytes < L.total)) return NF4_ERR_WORKSPACE;
+  if (!aligned16(ws)) return NF4_ERR_ALIGN;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (M == 0) {   // no tokens: the adapter gradients are zero
+    cudaError_t e = cudaMemsetAsync(dA, 0, sizeof(float) * static_cast<size_t>(rank) * K, cs);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dB, 0, sizeof(float) * static_cast<size_t>(N) * rank, cs);
+    return from_cuda(e);
+  }
+  char* w = static_cast<char*>(ws);
+  float* G = static_cast<float*>(ws);
+  const LinearArgs a{M, N, K, rank, s, w16 != nullptr ? Nf4View{} : view_of(W)};
+  cudaError_t e;
+  if (is16(compute)) {
+    int* status = nullptr;
+    if ((st = device_status_ptr(&status)) != NF4_OK) return st;
+    e = tc_backward(a, compute == NF4_F16, dy, nullptr, T, A, B, dx, nullptr, dB, G, w + L.tc, status, cs, w16);
+  } else {
+    const float* dyf = static_cast<const float*>(dy);
+    e = launch_lora_g(a, dyf, B, G, cs);
+    if (e == cudaSuccess) e = launch_dx_simt(a, dyf, G, A, static_cast<float*>(dx), cs);
+    if (e == cudaSuccess) e = launch_lora_dB(a, dyf, T, dB, cs);
+  }
+  if (e == cudaSuccess)
+    e = launch_act8_grad(ActGradArgs{M, K, rank, s, G, Act8View{x->codes, x->scales}, x_weight, dA}, w + L.part, cs);
+  return from_cuda(e);
 }
 
 nf4_status qlora_last_device_status(void* stream, int32_t clear) {

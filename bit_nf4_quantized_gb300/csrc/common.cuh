@@ -79,8 +79,15 @@ struct EncodeTables {
   int32_t sep_ok;
 };
 
+struct Nf4View;
+
 const DecodeTables& decode_tables();
 const EncodeTables& encode_tables();
+
+// abi.cu: the checks and lookups the entry points share.
+nf4_status device_status_word(int** out);
+nf4_status check_nf4_tensor(const nf4_tensor* t, int64_t numel);
+Nf4View nf4_view(const nf4_tensor* t);
 
 // Launch accounting (for the launch count reported by the ABI).
 void note_launch(int n = 1);

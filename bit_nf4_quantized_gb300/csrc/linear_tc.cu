@@ -936,6 +936,7 @@ cudaError_t tc_backward(const LinearArgs& a, bool f16, const void* dy, const voi
   if (e != cudaSuccess) return e;
   if ((e = gdb_pass(a, f16, dy, G, dB, L, w, w + L.Gt, pad8(a.M), status, st)) != cudaSuccess) return e;
   if ((e = dx_gemm(a, f16, dy, wb, w + L.ApT, w + L.sGp, part, w + L.flags, dx, status, st)) != cudaSuccess) return e;
+  if (x == nullptr) return cudaSuccess;   // the caller takes dA from G
   // dA = s G^T x: rows K, reduction over M down x's columns; written as [r][K]
   AdapterPassArgs da{};
   da.X = x;

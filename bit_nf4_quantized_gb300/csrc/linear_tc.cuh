@@ -15,6 +15,7 @@ size_t tc_bwd_ws_bytes(int64_t M, int64_t N, int64_t K, int r, bool w16 = false)
 // call then runs its operand staging alone instead of decoding a.W first.
 cudaError_t tc_forward(const LinearArgs& a, bool f16, const void* x, const float* A, const float* B, void* y,
                        float* T, void* ws, int* status, cudaStream_t st, const void* w16 = nullptr);
+// tc_backward with x == nullptr leaves dA to the caller, who finds G in fp32 in `G`.
 cudaError_t tc_backward(const LinearArgs& a, bool f16, const void* dy, const void* x, const float* T,
                         const float* A, const float* B, void* dx, float* dA, float* dB, float* G,
                         void* ws, int* status, cudaStream_t st, const void* w16 = nullptr);

@@ -342,6 +342,97 @@ size_t qlora_bwd_batch_workspace_bytes(int64_t M, int32_t count, const qlora_bwd
 nf4_status qlora_linear_bwd_batch(int64_t M, int32_t count, const qlora_bwd_item* items, nf4_dtype compute,
                                   void* ws, size_t ws_bytes, void* stream);
 
+/* ---- around the linear: the norm, 8-bit activation checkpoints, the loss -------------------- */
+
+/* An activation kept in 8 bits: int8 codes [rows, cols] row-major and one fp32 scale for each
+ * row and block of 128 columns, [rows, ceil(cols / 128)].  With amax the block's largest
+ * magnitude, scale = amax / 127, code = rint(x * (127 / amax)) in fp32 (ties to even), and the
+ * value read back is code * scale, at most scale / 2 (and rounding) from x.  A block with
+ * amax < 2^-116 is stored as zeros.  A block holding a NaN or an infinity gets the scale NaN,
+ * so that all of it reads back as NaN, and the device status word is set to
+ * NF4_ERR_NONFINITE. */
+typedef struct {
+  int64_t rows, cols;
+  int8_t* codes;          /* device, 16-byte aligned */
+  float* scales;          /* device, 16-byte aligned, qlora_act8_scales(rows, cols) values */
+} qlora_act8;
+
+/* rows * ceil(cols / 128); 0 for invalid sizes. */
+int64_t qlora_act8_scales(int64_t rows, int64_t cols);
+
+/* Store x (device [rows, cols] in dtype, any nf4_dtype) as out, and read it back:
+ * out[m][k] = code * scale (times weight[k] where weight, fp32 [cols], is given), computed in
+ * fp32 and rounded once to dtype.  Any cols >= 1; rows = 0 does nothing. */
+nf4_status qlora_act8_quantize(const void* x, nf4_dtype dtype, const qlora_act8* out, void* stream);
+nf4_status qlora_act8_dequantize(const qlora_act8* in, const float* weight, void* out, nf4_dtype dtype, void* stream);
+
+/* The A gradient of an adapter whose input is a checkpoint: with x = code * scale (times
+ * x_weight[k] where given, fp32 [cols]: a norm's weight behind the checkpoint of its normalised
+ * rows),
+ *     dA[j][k] = s sum_m G[m][j] x[m][k]        fp32 [rank, cols], overwritten
+ * G = dY B fp32 [rows, rank]; s from alpha, rank (1..256) and mode as for the linear.  The
+ * result is that of fp32 products and sums (no operand is rounded to 16 bits); the order of the
+ * sums is fixed.  rows = 0 gives zeros.  ws: qlora_act8_grad_a_workspace_bytes() bytes. */
+size_t qlora_act8_grad_a_workspace_bytes(int64_t M, int64_t K, int32_t rank);
+nf4_status qlora_act8_grad_a(int32_t rank, float alpha, qlora_scale_mode mode, const float* G, const qlora_act8* x,
+                             const float* x_weight, float* dA, void* ws, size_t ws_bytes, void* stream);
+
+/* qlora_linear_bwd (w16 == NULL) or qlora_linear_bwd_w16 (W may then be NULL) with x given as a
+ * checkpoint (and x_weight, as above): dX and dB are those calls' tensor-core or fp32 path,
+ * dA is qlora_act8_grad_a's.  x->rows = M and x->cols = K (NF4_ERR_SHAPE otherwise).
+ * ws: qlora_bwd_act8_workspace_bytes() bytes (w16: whether the weight is given decoded). */
+size_t qlora_bwd_act8_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t rank, nf4_dtype compute, int32_t w16);
+nf4_status qlora_linear_bwd_act8(int64_t M, int64_t N, int64_t K, int32_t rank, float alpha, qlora_scale_mode mode,
+                                 nf4_dtype compute, const void* dy, const qlora_act8* x, const float* x_weight,
+                                 const float* T, const nf4_tensor* W, const void* w16, const float* A, const float* B,
+                                 void* dx, float* dA, float* dB, void* ws, size_t ws_bytes, void* stream);
+
+/* RMS norm with the residual's addition, over rows of K:
+ *     h = x + residual,  rstd = 1 / sqrt(mean_k h^2 + eps),  n = h rstd,  y = n weight
+ * x, residual, y, h: device [M, K] in dtype (any nf4_dtype); weight fp32 [K]; rstd fp32 [M].
+ * residual may be NULL (h = x), h may be NULL (not stored), checkpoint may be NULL; given, n is
+ * stored in it (before the weight, so that one checkpoint serves the norm's backward pass and,
+ * with x_weight = weight, the adapters behind the norm).  fp32 arithmetic; y and h are rounded
+ * once, y from the unrounded sum.  y may be x or residual, h likewise, where the pointers are
+ * equal.  eps >= 0 finite.  Any K >= 1; M = 0 does nothing. */
+nf4_status qlora_rms_norm_fwd(int64_t M, int64_t K, float eps, nf4_dtype dtype, const void* x, const void* residual,
+                              const float* weight, void* y, void* h, float* rstd, const qlora_act8* checkpoint,
+                              void* stream);
+
+/* Its backward pass, from the forward's rstd and either h or the checkpoint (exactly one):
+ *     n = h rstd  (or the checkpoint's values),   d = dy weight
+ *     dx = rstd (d - n mean_k(d n)) + dresidual,       dweight = sum_m dy n
+ * dy, h, dresidual, dx: device [M, K] in dtype; dresidual (the gradient that reaches h by the
+ * residual path) and dweight (fp32 [K], overwritten) may be NULL.  dx is the gradient of x and
+ * of residual alike; it may be dresidual's or dy's buffer.  The order of dweight's sums is
+ * fixed.  ws: qlora_rms_norm_bwd_workspace_bytes() bytes, needed with dweight. */
+size_t qlora_rms_norm_bwd_workspace_bytes(int64_t M, int64_t K);
+nf4_status qlora_rms_norm_bwd(int64_t M, int64_t K, nf4_dtype dtype, const void* dy, const void* h,
+                              const qlora_act8* checkpoint, const float* rstd, const float* weight,
+                              const void* dresidual, void* dx, float* dweight, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* Softmax cross entropy of a frozen head, and its gradient, without keeping the logits:
+ *     z = x W^T,   lse[m] = log sum_v exp z[m][v],   loss[m] = lse[m] - z[m][targets[m]]
+ *     dx[m] = g[m] (softmax(z[m]) - onehot(targets[m])) W
+ * x [M, D] and dx in the compute dtype (NF4_BF16 or NF4_F16; NF4_ERR_DTYPE otherwise); the head
+ * is w16 [V, D] in the compute dtype, or, with w16 == NULL, the nf4_tensor W of numel V*D, of
+ * which only a piece is decoded at a time.  D >= 64 and D % 8 == 0 (D % 64 == 0 for W); any
+ * V >= 1.  targets: device int64 [M].  A token whose target is ignore_index does not count: its
+ * loss, lse and dx are zero.  So are those of a token whose target is otherwise outside [0, V),
+ * and the device status word is set to NF4_ERR_ARG.
+ * grad_scale: device fp32, [M] with grad_scale_per_row != 0, else [1]; NULL means 1.  lse may be
+ * NULL.  dx == NULL computes no gradient (2 M V D operations instead of 4 M V D).
+ * Logits, exponentials and sums are fp32; the 16-bit roundings are those of the exponentials
+ * that the tensor cores multiply with W (the target's own term is not rounded) and dx itself.
+ * Deterministic.  ws: qlora_lm_loss_workspace_bytes() bytes (stored: the head is an
+ * nf4_tensor; gradient: dx is asked for). */
+size_t qlora_lm_loss_workspace_bytes(int64_t M, int64_t V, int64_t D, int32_t stored, int32_t gradient);
+nf4_status qlora_lm_loss(int64_t M, int64_t V, int64_t D, nf4_dtype compute, const void* x, const nf4_tensor* W,
+                         const void* w16, const int64_t* targets, int64_t ignore_index, const float* grad_scale,
+                         int32_t grad_scale_per_row, float* loss, float* lse, void* dx, void* ws, size_t ws_bytes,
+                         void* stream);
+
 /* Synchronize `stream`, then return the current device's status word (NF4_OK if no
  * device-side condition was recorded); clear != 0 resets it to NF4_OK. */
 nf4_status qlora_last_device_status(void* stream, int32_t clear);
