@@ -1,7 +1,10 @@
 // 8-bit activation checkpoints: storing, reading back, and the adapter gradient
 // dA = s G^T x taken straight from the codes.
 #include <algorithm>
+#include <mutex>
+#include <type_traits>
 
+#include "mma_sync.cuh"
 #include "train_ops.cuh"
 
 namespace qnf4 {
@@ -72,64 +75,284 @@ cudaError_t dequantize_t(Act8View in, int64_t M, int64_t K, const float* weight,
 }
 
 // ---- dA ---------------------------------------------------------------------------------
-constexpr int kGradRanks = 16;     // ranks of a CTA
-constexpr int kGradTokens = 64;    // tokens staged at a time
+//
+// dA[j][k] = s w[k] sum_m (G[m][j] scale[m][k / 128]) code[m][k].  The codes are exact in half,
+// and p = G scale 2^e (e keeps |p| < 2^15) is split as hi + lo, two halves of 11 bits each, so
+// the products are those of 22-bit operands and the sums are the tensor cores' fp32.  (With
+// p in one half, or one bf16 as the adapter passes of the linear have it, dA would carry that
+// rounding; two bf16 halves give 16 bits and three cost half as much again.)
+//
+// A CTA owns 512 features, one block of 128 (one scale a token) for each of its four warps, and
+// 16 ranks: m16n8k16 products with the ranks as M, 16 tokens as K, and 16 times 8 features as N.
+// A lane reads 16 neighbouring codes of 4 tokens and turns them into B fragments in registers:
+// product i takes column i of every lane's 16, and lane 4 g + q takes tokens q, q + 4, q + 8,
+// q + 12 (any order of a sum's terms will do), so that the shared-memory reads meet no bank
+// twice.  The sums hold 64 of a thread's 128 registers, which leaves none for loads in flight:
+// a ring of cp.async stages (codes, G and scales of 16 tokens) carries them instead.
+//
+// Rows of codes start at any byte when K % 16 != 0; the copies then take whole aligned 16-byte
+// pieces of the flat array, and a lane shifts its 16 codes into place.
+//
+// e belongs to the warp and falls when a step's largest |G scale| would leave half's range; the
+// sums then fall with it, and are put back into fp32's own scale at the end.  Tokens are cut in
+// slices, whose sums a second launch adds in order.
+constexpr int kGradRanks = 16;
+constexpr int kGradWarps = 4;                                  // one block of 128 features each
+constexpr int kGradThreads = kGradWarps * 32;
+constexpr int kGradCols = kGradWarps * kActBlock;
+constexpr int kGradCtas = 4;                                   // resident on an SM
+constexpr int kCodePitch = kGradCols + 32;                     // bytes: 4 rows x 32 bytes on 32 banks
+constexpr int kGPitch = 24;                                    // floats: 4 rows x 8 ranks on 32 banks
+constexpr int kRingCodes = 16 * kCodePitch, kRingG = 16 * kGPitch * 4, kRingS = 16 * kGradWarps * 4;
+constexpr int kRingBytes = kRingCodes + kRingG + kRingS;       // 10496
+constexpr int kRing = 5;
+constexpr int kGradSmem = kRing * kRingBytes;
 
-// One block of 128 features (a thread each), 16 ranks, one slice of the tokens: fp32 products
-// and sums.  part: [slice][r][K].
-__global__ void act8_grad(const ActGradArgs a, int64_t slice_tokens, float* part) {
-  __shared__ float g[kGradTokens][kGradRanks];
-  __shared__ float sc[kGradTokens];
+__device__ __forceinline__ uint32_t smem_at(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+// 16 (or 4) bytes to shared memory, of which the last 16 - n (4 - n) are zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// Two codes (bytes 0 and 2 of w, or with kHigh 1 and 3) as halves: 0x64cc with the code's sign
+// bit flipped is 1024 + 128 + code.
+template <bool kHigh>
+__device__ __forceinline__ uint32_t codes_half2(uint32_t w) {
+  const uint32_t b = kHigh ? w >> 8 : w;
+  uint32_t h, out;
+  asm("lop3.b32 %0, %1, 0x00ff00ff, 0x64806480, 0x6a;" : "=r"(h) : "r"(b));   // (b & m) ^ c
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(out) : "r"(h), "r"(0x64806480u));
+  return out;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <bool kVec>
+__global__ void __launch_bounds__(kGradThreads, kGradCtas)
+act8_grad(const ActGradArgs a, int slice_steps, int slices, float* part) {
+  extern __shared__ __align__(16) uint8_t ring[];
   pdl_allow_next();
   pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, q = lane & 3;
   const int64_t nb = (a.K + kActBlock - 1) / kActBlock;
-  const int64_t k = static_cast<int64_t>(blockIdx.x) * kActBlock + threadIdx.x;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kGradCols, b0 = static_cast<int64_t>(blockIdx.x) * kGradWarps;
   const int j0 = blockIdx.z * kGradRanks;
-  const int64_t m0 = blockIdx.y * slice_tokens, m1 = min(m0 + slice_tokens, a.M);
-  float acc[kGradRanks];
+  const int64_t steps = (a.M + 15) / 16;
+  const int64_t s0 = blockIdx.y * static_cast<int64_t>(slice_steps), s1 = min(s0 + slice_steps, steps);
+  const int n_steps = static_cast<int>(s1 - s0);
+  const uint32_t ring0 = smem_at(ring);
+  const int64_t bytes = a.M * a.K;
+  const int64_t row_end = min(c0 + kGradCols, a.K);     // the features of this CTA's rows end here
+
+  // The copies of step st (or an empty group past the slice's end).
+  auto issue = [&](int st) {
+    if (st < n_steps) {
+      const uint32_t dst = ring0 + (st % kRing) * kRingBytes;
+      const int64_t m0 = (s0 + st) * 16;
+      if (kVec) {
 #pragma unroll
-  for (int j = 0; j < kGradRanks; ++j) acc[j] = 0.0f;
-  for (int64_t mb = m0; mb < m1; mb += kGradTokens) {
-    const int n = static_cast<int>(min(static_cast<int64_t>(kGradTokens), m1 - mb));
-    __syncthreads();
-    for (int i = threadIdx.x; i < n * kGradRanks; i += kActBlock) {
-      const int t = i / kGradRanks, j = i % kGradRanks;
-      g[t][j] = j0 + j < a.r ? a.G[(mb + t) * a.r + j0 + j] : 0.0f;
+        for (int i = 0; i < 4; ++i) {   // 32 pieces a row, 4 rows at a time
+          const int row = i * 4 + (threadIdx.x >> 5), piece = threadIdx.x & 31;
+          const int64_t m = m0 + row, c = c0 + 16 * piece;
+          const bool in = m < a.M && c < row_end;
+          copy16(dst + row * kCodePitch + 16 * piece, a.act.codes + (in ? m * a.K + c : 0), in ? 16 : 0);
+        }
+      } else {
+        for (int i = threadIdx.x; i < 16 * 33; i += kGradThreads) {
+          const int row = i / 33, piece = i - row * 33;
+          const int64_t m = m0 + row;
+          const int64_t at = ((m * a.K + c0) & ~int64_t(15)) + 16 * piece;
+          const int64_t left = min(int64_t(16), bytes - at);
+          const bool in = m < a.M && at < m * a.K + row_end;
+          copy16(dst + row * kCodePitch + 16 * piece, a.act.codes + (in ? at : 0), in ? static_cast<int>(left) : 0);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = i * 8 + (threadIdx.x >> 4), j = threadIdx.x & 15;
+        const int64_t m = m0 + row;
+        const bool in = m < a.M && j0 + j < a.r;
+        copy4(dst + kRingCodes + (row * kGPitch + j) * 4, a.G + (in ? m * a.r + j0 + j : 0), in ? 4 : 0);
+      }
+      if (threadIdx.x < 16 * kGradWarps) {
+        const int row = threadIdx.x / kGradWarps, b = threadIdx.x % kGradWarps;
+        const int64_t m = m0 + row;
+        const bool in = m < a.M && b0 + b < nb;
+        copy4(dst + kRingCodes + kRingG + threadIdx.x * 4, a.act.scales + (in ? m * nb + b0 + b : 0), in ? 4 : 0);
+      }
     }
-    if (threadIdx.x < n) sc[threadIdx.x] = a.act.scales[(mb + threadIdx.x) * nb + blockIdx.x];
-    __syncthreads();
-    if (k < a.K) {
-      for (int t = 0; t < n; ++t) {
-        const float x = static_cast<float>(a.act.codes[(mb + t) * a.K + k]) * sc[t];
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  float acc[16][4];
 #pragma unroll
-        for (int j = 0; j < kGradRanks; ++j) acc[j] = fmaf(g[t][j], x, acc[j]);
+  for (int i = 0; i < 16; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
+  int e = 126;
+  for (int st = 0; st < kRing - 1; ++st) issue(st);
+  for (int st = 0; st < n_steps; ++st) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+    __syncthreads();             // everyone's copies of this step, and everyone has left the stage refilled next
+    issue(st + kRing - 1);
+    const uint8_t* stage = ring + (st % kRing) * kRingBytes;
+    const float* gs = reinterpret_cast<const float*>(stage + kRingCodes);
+    const float* ss = reinterpret_cast<const float*>(stage + kRingCodes + kRingG);
+    float p[2][4];
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float sc = ss[(q + 4 * i) * kGradWarps + warp];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) p[h][i] = gs[(q + 4 * i) * kGPitch + g + 8 * h] * sc, top = fmaxf(top, fabsf(p[h][i]));
+    }
+    const unsigned topw = __reduce_max_sync(0xffffffffu, __float_as_uint(top));   // non-negative: ordered as bits
+    const int ex = static_cast<int>(topw >> 23) - 127;      // |p| < 2^(ex + 1)
+    if (ex + 1 + e > 15) {
+      const int down = max(10 - ex, -126);
+      const float f = ldexpf(1.0f, down - e);
+      e = down;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][k] *= f;
+    }
+    const float up = __int_as_float((e + 127) << 23);
+    uint32_t hi[4], lo[4];     // a0: rank g, the lane's tokens 0 1; a1: rank g + 8; a2, a3: tokens 2 3
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float u = p[h][2 * i] * up, v = p[h][2 * i + 1] * up;
+        const uint32_t b = half2_bits(u, v);
+        hi[2 * i + h] = b;
+        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&b));
+        lo[2 * i + h] = half2_bits(u - back.x, v - back.y);
+      }
+    uint4 code[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = q + 4 * i;
+      const uint8_t* src = stage + row * kCodePitch + warp * kActBlock + 16 * g;
+      if (kVec) {
+        code[i] = *reinterpret_cast<const uint4*>(src);
+      } else {
+        const uint32_t off = static_cast<uint32_t>(((s0 + st) * 16 + row) * a.K + c0) & 15u;   // row's first byte
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(src + (off & ~3u));
+        const uint32_t sh = (off & 3u) * 8;
+        const uint32_t w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3], w4 = w[4];
+        code[i] = make_uint4(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh), __funnelshift_r(w2, w3, sh),
+                             __funnelshift_r(w3, w4, sh));
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      uint32_t t[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] = w == 0 ? code[i].x : w == 1 ? code[i].y : w == 2 ? code[i].z : code[i].w;
+      // columns 4w, 4w + 1 of tokens 0 1 and 2 3, then columns 4w + 2, 4w + 3
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t sel = c == 0 ? 0x5410u : 0x7632u;
+        const uint32_t x01 = __byte_perm(t[0], t[1], sel), x23 = __byte_perm(t[2], t[3], sel);
+        const uint32_t b00 = codes_half2<false>(x01), b01 = codes_half2<false>(x23);
+        const uint32_t b10 = codes_half2<true>(x01), b11 = codes_half2<true>(x23);
+        const int n = 4 * w + 2 * c;
+        mma16816<true>(acc[n], hi[0], hi[1], hi[2], hi[3], b00, b01);
+        mma16816<true>(acc[n + 1], hi[0], hi[1], hi[2], hi[3], b10, b11);
+        mma16816<true>(acc[n], lo[0], lo[1], lo[2], lo[3], b00, b01);
+        mma16816<true>(acc[n + 1], lo[0], lo[1], lo[2], lo[3], b10, b11);
       }
     }
   }
-  if (k < a.K) {
+  // acc[n][k]: rank g + 8 (k / 2), feature 32 q + 16 (k % 2) + n of the warp's block, times 2^e
+  const float back = __int_as_float((127 - e) << 23);
+  const bool direct = slices == 1;
+  float* dst = direct ? a.dA : part + static_cast<int64_t>(blockIdx.y) * a.r * a.K;
 #pragma unroll
-    for (int j = 0; j < kGradRanks; ++j)
-      if (j0 + j < a.r) part[(static_cast<int64_t>(blockIdx.y) * a.r + j0 + j) * a.K + k] = acc[j];
+  for (int k = 0; k < 4; ++k) {
+    const int rank = j0 + g + 8 * (k / 2);
+    if (rank >= a.r) continue;
+    float* row = dst + rank * a.K;
+#pragma unroll
+    for (int n = 0; n < 16; n += 4) {
+      const int64_t kk = c0 + warp * kActBlock + 32 * q + 16 * (k % 2) + n;
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = acc[n + i][k] * back;
+        if (direct) v[i] = v[i] * a.s * (a.weight != nullptr && kk + i < a.K ? a.weight[kk + i] : 1.0f);
+      }
+      if (kVec) {
+        if (kk < a.K) *reinterpret_cast<float4*>(row + kk) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (kk + i < a.K) row[kk + i] = v[i];
+      }
+    }
   }
 }
 
-// dA = s * weight * (the slices' sums in order)
+// dA = s * weight * (the slices' sums in order), kW values a thread.
+template <int kW>
 __global__ void act8_grad_finish(const ActGradArgs a, const float* part, int slices) {
   pdl_allow_next();
   pdl_wait();
   const int64_t n = static_cast<int64_t>(a.r) * a.K;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * kW;
   if (i >= n) return;
-  float s = 0.0f;
-  for (int q = 0; q < slices; ++q) s += part[q * n + i];
-  s *= a.s;
-  a.dA[i] = a.weight != nullptr ? s * a.weight[i % a.K] : s;
+  using V = typename std::conditional<kW == 4, float4, float>::type;
+  float v[kW];
+#pragma unroll
+  for (int k = 0; k < kW; ++k) v[k] = 0.0f;
+#pragma unroll 8
+  for (int y = 0; y < slices; ++y) {
+    const V u = __ldcg(reinterpret_cast<const V*>(part + y * n + i));
+#pragma unroll
+    for (int k = 0; k < kW; ++k) v[k] += reinterpret_cast<const float*>(&u)[k];
+  }
+  const int64_t kk = i % a.K;    // K % kW == 0: the values share a row
+#pragma unroll
+  for (int k = 0; k < kW; ++k) a.dA[i + k] = v[k] * a.s * (a.weight != nullptr ? a.weight[kk + k] : 1.0f);
 }
 
+// Slices of the tokens: the count with the least time, in units of a quarter of a step: rounds of
+// resident CTAs times their steps and 4 steps' worth for a CTA's own ends, and with several
+// slices 6 steps for the launch that adds them and a quarter for reading each.
 int grad_slices(int64_t M, int64_t K, int r) {
-  const int64_t ctas = (K + kActBlock - 1) / kActBlock * ((r + kGradRanks - 1) / kGradRanks);
-  const int64_t want = (device_sm_count() * 8 + ctas - 1) / ctas;
-  return static_cast<int>(std::max<int64_t>(1, std::min({want, (M + kGradTokens - 1) / kGradTokens, int64_t(64)})));
+  const int64_t groups = (K + kGradCols - 1) / kGradCols * ((r + kGradRanks - 1) / kGradRanks);
+  const int64_t steps = (M + 15) / 16, slots = kGradCtas * static_cast<int64_t>(device_sm_count());
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int s = 1; s <= 64 && s <= steps; ++s) {
+    const int64_t per = (steps + s - 1) / s;
+    const int64_t rounds = (groups * s + slots - 1) / slots;
+    const int64_t cost = 4 * rounds * (per + 4) + (s > 1 ? 24 + s : 0);
+    if (cost < best_cost) best = s, best_cost = cost;
+  }
+  return best;
+}
+
+template <bool kVec>
+cudaError_t launch_grad(const ActGradArgs& a, dim3 grid, int per, int slices, float* part, cudaStream_t st) {
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [&] {
+    err = cudaFuncSetAttribute(act8_grad<kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
+  });
+  if (err != cudaSuccess) return err;
+  note_launch();
+  return launch_pdl(act8_grad<kVec>, grid, dim3(kGradThreads), kGradSmem, st, 1, a, per, slices, part);
 }
 
 }  // namespace
@@ -161,18 +384,20 @@ size_t act8_grad_ws_bytes(int64_t M, int64_t K, int r) {
 cudaError_t launch_act8_grad(const ActGradArgs& a, void* ws, cudaStream_t st) {
   if (a.M == 0) return cudaMemsetAsync(a.dA, 0, sizeof(float) * static_cast<size_t>(a.r) * a.K, st);
   const int want = grad_slices(a.M, a.K, a.r);
-  const int64_t per = (a.M + want - 1) / want;
-  const int slices = static_cast<int>((a.M + per - 1) / per);
-  auto* part = static_cast<float*>(ws);
-  const dim3 grid(static_cast<unsigned>((a.K + kActBlock - 1) / kActBlock), static_cast<unsigned>(slices),
+  const int64_t steps = (a.M + 15) / 16, per = (steps + want - 1) / want;
+  const int slices = static_cast<int>((steps + per - 1) / per);
+  const dim3 grid(static_cast<unsigned>((a.K + kGradCols - 1) / kGradCols), static_cast<unsigned>(slices),
                   static_cast<unsigned>((a.r + kGradRanks - 1) / kGradRanks));
+  auto* part = static_cast<float*>(ws);
+  const cudaError_t e = a.K % 16 == 0 ? launch_grad<true>(a, grid, static_cast<int>(per), slices, part, st)
+                                      : launch_grad<false>(a, grid, static_cast<int>(per), slices, part, st);
+  if (e != cudaSuccess || slices == 1) return e;
+  const int w = a.K % 4 == 0 ? 4 : 1;
+  const int64_t n = static_cast<int64_t>(a.r) * a.K / w;
+  const dim3 fgrid(static_cast<unsigned>((n + kThreads - 1) / kThreads));
   note_launch();
-  cudaError_t e = launch_pdl(act8_grad, grid, dim3(kActBlock), 0, st, 1, a, per, part);
-  if (e != cudaSuccess) return e;
-  const int64_t n = static_cast<int64_t>(a.r) * a.K;
-  note_launch();
-  return launch_pdl(act8_grad_finish, dim3(static_cast<unsigned>((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
-                    1, a, static_cast<const float*>(part), slices);
+  return w == 4 ? launch_pdl(act8_grad_finish<4>, fgrid, dim3(kThreads), 0, st, 1, a, static_cast<const float*>(part), slices)
+                : launch_pdl(act8_grad_finish<1>, fgrid, dim3(kThreads), 0, st, 1, a, static_cast<const float*>(part), slices);
 }
 
 }  // namespace qnf4
