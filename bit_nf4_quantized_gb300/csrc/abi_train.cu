@@ -133,7 +133,9 @@ nf4_status qlora_rms_norm_bwd(int64_t M, int64_t K, nf4_dtype dtype, const void*
   if (need > 0 && !aligned16(ws)) return NF4_ERR_ALIGN;
   const NormBwdArgs a{M, K, dy, h, checkpoint != nullptr ? Act8View{checkpoint->codes, checkpoint->scales} : Act8View{},
                       rstd, weight, dresidual, dx, dweight, static_cast<float*>(ws)};
-  return from_cuda(launch_rms_norm_bwd(a, dtype, static_cast<cudaStream_t>(stream)));
+  int* status = nullptr;
+  if ((st = device_status_word(&status)) != NF4_OK) return st;
+  return from_cuda(launch_rms_norm_bwd(a, dtype, status, static_cast<cudaStream_t>(stream)));
 }
 
 size_t qlora_lm_loss_workspace_bytes(int64_t M, int64_t V, int64_t D, int32_t stored, int32_t gradient) {

@@ -12,61 +12,91 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// One lane per 8 values, 16 lanes per block (train_ops.cuh).  Bound by HBM: the activation
-// once, one byte a value and 4 / 128 out.
+// A thread's chunks of 8 values: kPer of them, kThreads apart, as (row, chunk of the row).  One
+// division a thread; the rest is counted up.
+constexpr int kPer = 4;
+struct ChunkWalk {
+  int64_t m, c;
+  __device__ __forceinline__ ChunkWalk(int64_t i, int64_t C) {
+    if (i <= 0xffffffffLL) {
+      const uint32_t row = static_cast<uint32_t>(i) / static_cast<uint32_t>(C);
+      m = row, c = i - row * C;
+    } else {
+      m = i / C, c = i - m * C;
+    }
+  }
+  __device__ __forceinline__ void next(int64_t C) {
+    for (c += kThreads; c >= C; c -= C) ++m;
+  }
+};
+
+// Four lanes to a block of 128, 32 values each (train_ops.cuh): with 8 values a lane the block's
+// reduction and divisions took longer than its bytes (4096 x 14336 bf16: 51 us; with 32, 29 us,
+// 0.91 of the measured copy bandwidth).  Rows that are not 16-byte aligned keep 8 values a lane,
+// whose narrow accesses then share sectors (4096 x 4095: 27 us; with 32 a lane, 45).  Bound by
+// HBM: the activation once, one byte a value and 4 / 128 out.
+template <bool kVec>
+constexpr int quant_chunks() { return kVec ? 4 : 1; }
 template <typename T, bool kVec>
-__global__ void act8_quantize(const T* x, int64_t M, int64_t K, Act8View out, int* status) {
+__global__ void __launch_bounds__(kThreads) act8_quantize(const T* x, int64_t M, int64_t K, Act8View out, int* status) {
+  constexpr int kN = quant_chunks<kVec>();
   pdl_allow_next();
   pdl_wait();
-  const int64_t C = (K + kActBlock - 1) / kActBlock * kActLanes;
-  const int64_t n = M * C;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const bool on = i < n;     // whole blocks of 16 lanes
-  const int64_t m = on ? i / C : 0, c = on ? i - m * C : 0;
-  float v[8];
-  load8<T, kVec>(x + m * K, c, K, v);
-  const Quantized q = quantize_block(v);
-  if (on) store_codes<kVec>(out, m, c, K, q);
-  if (on && q.bad) atomicCAS(status, 0, static_cast<int>(NF4_ERR_NONFINITE));
+  const int64_t L = (K + kActBlock - 1) / kActBlock * (kActLanes / kN);   // lanes of a row
+  const ChunkWalk w(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, L);
+  float v[kN][8];
+#pragma unroll
+  for (int u = 0; u < kN; ++u) {
+    if (w.m < M) load8<T, kVec>(x + w.m * K, chunk_of(w.c, kN, u), K, v[u]);
+    else
+      for (int j = 0; j < 8; ++j) v[u][j] = 0.0f;
+  }
+  const Quantized<kN> q = quantize_block<kN>(v);
+  if (w.m < M) store_block<kVec, kN>(out, w.m, w.c, K, q, status);
 }
 
 template <typename T, bool kVec>
-__global__ void act8_dequantize(Act8View in, int64_t M, int64_t K, const float* weight, T* out) {
+__global__ void __launch_bounds__(kThreads) act8_dequantize(Act8View in, int64_t M, int64_t K, const float* weight, T* out) {
   pdl_allow_next();
   pdl_wait();
   const int64_t C = (K + kActBlock - 1) / kActBlock * kActLanes, nb = C / kActLanes;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= M * C) return;
-  const int64_t m = i / C, c = i - m * C;
-  const uint2 q = load_codes<kVec>(in.codes + m * K, c, K);
-  const float sc = in.scales[m * nb + c / kActLanes];
-  float v[8];
+  ChunkWalk w(static_cast<int64_t>(blockIdx.x) * (kThreads * kPer) + threadIdx.x, C), at = w;
+  uint2 q[kPer];
+  float sc[kPer];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = code_value(q, j) * sc;
-  if (weight != nullptr) {
-    float w[8];
-    load8<float, kVec>(weight, c, K, w);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= w[j];
+  for (int u = 0; u < kPer; ++u, at.next(C)) {
+    const int64_t m = min(at.m, M - 1);
+    q[u] = load_codes<kVec>(in.codes + m * K, at.c, K);
+    sc[u] = in.scales[m * nb + at.c / kActLanes];
   }
-  store8<T, kVec>(out + m * K, c, K, v);
+#pragma unroll
+  for (int u = 0; u < kPer; ++u, w.next(C)) {
+    if (w.m >= M) continue;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = code_value(q[u], j) * sc[u];
+    if (weight != nullptr) {
+      float g[8];
+      load8<float, kVec>(weight, w.c, K, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= g[j];
+    }
+    store8<T, kVec>(out + w.m * K, w.c, K, v);
+  }
 }
 
-template <typename T>
+template <typename T, bool kVec>
 cudaError_t quantize_t(const void* x, int64_t M, int64_t K, Act8View out, int* status, cudaStream_t st) {
-  const int64_t n = M * ((K + kActBlock - 1) / kActBlock) * kActLanes;
-  const dim3 grid(static_cast<unsigned>((n + kThreads - 1) / kThreads));
+  const int64_t n = M * ((K + kActBlock - 1) / kActBlock) * (kActLanes / quant_chunks<kVec>());
   note_launch();
-  return K % 8 == 0 ? launch_pdl(act8_quantize<T, true>, grid, dim3(kThreads), 0, st, 1, static_cast<const T*>(x), M, K,
-                                 out, status)
-                    : launch_pdl(act8_quantize<T, false>, grid, dim3(kThreads), 0, st, 1, static_cast<const T*>(x), M,
-                                 K, out, status);
+  return launch_pdl(act8_quantize<T, kVec>, dim3(static_cast<unsigned>((n + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+                    st, 1, static_cast<const T*>(x), M, K, out, status);
 }
 
 template <typename T>
 cudaError_t dequantize_t(Act8View in, int64_t M, int64_t K, const float* weight, void* out, cudaStream_t st) {
   const int64_t n = M * ((K + kActBlock - 1) / kActBlock) * kActLanes;
-  const dim3 grid(static_cast<unsigned>((n + kThreads - 1) / kThreads));
+  const dim3 grid(static_cast<unsigned>((n + kThreads * kPer - 1) / (kThreads * kPer)));
   note_launch();
   return K % 8 == 0 ? launch_pdl(act8_dequantize<T, true>, grid, dim3(kThreads), 0, st, 1, in, M, K, weight,
                                  static_cast<T*>(out))
@@ -153,41 +183,55 @@ act8_grad(const ActGradArgs a, int slice_steps, int slices, float* part) {
   const int64_t bytes = a.M * a.K;
   const int64_t row_end = min(c0 + kGradCols, a.K);     // the features of this CTA's rows end here
 
+  // This thread's part of a stage's copies: its sources for the slice's first step, which move on
+  // by 16 tokens a step.  A copy of no bytes (past the last token, feature, rank or block) only
+  // writes zeros.
+  const int64_t m00 = s0 * 16;
+  const int row4 = threadIdx.x >> 5, piece = threadIdx.x & 31;    // kVec: 32 pieces a row, 4 rows at a time
+  const bool col_in = c0 + 16 * piece < row_end;
+  const int8_t* code_src = a.act.codes + (m00 + row4) * a.K + c0 + 16 * piece;
+  const uint32_t code_dst = ring0 + row4 * kCodePitch + 16 * piece;
+  const int grow = threadIdx.x >> 4, gj = threadIdx.x & 15;       // G: 16 ranks a row, 8 rows at a time
+  const bool rank_in = j0 + gj < a.r;
+  const float* g_src = a.G + (m00 + grow) * a.r + j0 + gj;
+  const uint32_t g_dst = ring0 + kRingCodes + (grow * kGPitch + gj) * 4;
+  const int srow = threadIdx.x / kGradWarps, sb = threadIdx.x % kGradWarps;
+  const bool blk_in = srow < 16 && b0 + sb < nb;
+  const float* s_src = a.act.scales + (m00 + srow) * nb + b0 + sb;
+  const uint32_t s_dst = ring0 + kRingCodes + kRingG + threadIdx.x * 4;
   // The copies of step st (or an empty group past the slice's end).
-  auto issue = [&](int st) {
+  auto issue = [&](int st, int slot) {
     if (st < n_steps) {
-      const uint32_t dst = ring0 + (st % kRing) * kRingBytes;
-      const int64_t m0 = (s0 + st) * 16;
+      const uint32_t at = slot * kRingBytes;
+      const int left = static_cast<int>(min(int64_t(16), a.M - m00 - 16 * static_cast<int64_t>(st)));   // tokens of the step
       if (kVec) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {   // 32 pieces a row, 4 rows at a time
-          const int row = i * 4 + (threadIdx.x >> 5), piece = threadIdx.x & 31;
-          const int64_t m = m0 + row, c = c0 + 16 * piece;
-          const bool in = m < a.M && c < row_end;
-          copy16(dst + row * kCodePitch + 16 * piece, a.act.codes + (in ? m * a.K + c : 0), in ? 16 : 0);
+        for (int i = 0; i < 4; ++i) {
+          const bool in = col_in && row4 + 4 * i < left;
+          copy16(code_dst + at + 4 * i * kCodePitch, in ? code_src + 4 * i * a.K : a.act.codes, in ? 16 : 0);
         }
+        code_src += 16 * a.K;
       } else {
+        const int64_t m0 = m00 + 16 * static_cast<int64_t>(st);
         for (int i = threadIdx.x; i < 16 * 33; i += kGradThreads) {
-          const int row = i / 33, piece = i - row * 33;
+          const int row = i / 33, pc = i - row * 33;
           const int64_t m = m0 + row;
-          const int64_t at = ((m * a.K + c0) & ~int64_t(15)) + 16 * piece;
-          const int64_t left = min(int64_t(16), bytes - at);
-          const bool in = m < a.M && at < m * a.K + row_end;
-          copy16(dst + row * kCodePitch + 16 * piece, a.act.codes + (in ? at : 0), in ? static_cast<int>(left) : 0);
+          const int64_t byte = ((m * a.K + c0) & ~int64_t(15)) + 16 * pc;
+          const bool in = row < left && byte < m * a.K + row_end;
+          copy16(ring0 + at + row * kCodePitch + 16 * pc, a.act.codes + (in ? byte : 0),
+                 in ? static_cast<int>(min(int64_t(16), bytes - byte)) : 0);
         }
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int row = i * 8 + (threadIdx.x >> 4), j = threadIdx.x & 15;
-        const int64_t m = m0 + row;
-        const bool in = m < a.M && j0 + j < a.r;
-        copy4(dst + kRingCodes + (row * kGPitch + j) * 4, a.G + (in ? m * a.r + j0 + j : 0), in ? 4 : 0);
+        const bool in = rank_in && grow + 8 * i < left;
+        copy4(g_dst + at + 8 * i * kGPitch * 4, in ? g_src + 8 * i * a.r : a.G, in ? 4 : 0);
       }
-      if (threadIdx.x < 16 * kGradWarps) {
-        const int row = threadIdx.x / kGradWarps, b = threadIdx.x % kGradWarps;
-        const int64_t m = m0 + row;
-        const bool in = m < a.M && b0 + b < nb;
-        copy4(dst + kRingCodes + kRingG + threadIdx.x * 4, a.act.scales + (in ? m * nb + b0 + b : 0), in ? 4 : 0);
+      g_src += 16 * a.r;
+      if (srow < 16) {
+        const bool in = blk_in && srow < left;
+        copy4(s_dst + at, in ? s_src : a.act.scales, in ? 4 : 0);
+        s_src += 16 * nb;
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -199,12 +243,13 @@ act8_grad(const ActGradArgs a, int slice_steps, int slices, float* part) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
   int e = 126;
-  for (int st = 0; st < kRing - 1; ++st) issue(st);
-  for (int st = 0; st < n_steps; ++st) {
+  for (int st = 0; st < kRing - 1; ++st) issue(st, st);
+  int slot = 0;
+  for (int st = 0; st < n_steps; ++st, slot = slot + 1 == kRing ? 0 : slot + 1) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
     __syncthreads();             // everyone's copies of this step, and everyone has left the stage refilled next
-    issue(st + kRing - 1);
-    const uint8_t* stage = ring + (st % kRing) * kRingBytes;
+    issue(st + kRing - 1, slot == 0 ? kRing - 1 : slot - 1);
+    const uint8_t* stage = ring + slot * kRingBytes;
     const float* gs = reinterpret_cast<const float*>(stage + kRingCodes);
     const float* ss = reinterpret_cast<const float*>(stage + kRingCodes + kRingG);
     float p[2][4];
@@ -360,10 +405,15 @@ cudaError_t launch_grad(const ActGradArgs& a, dim3 grid, int per, int slices, fl
 cudaError_t launch_act8_quantize(const void* x, nf4_dtype dt, int64_t M, int64_t K, Act8View out, int* status,
                                  cudaStream_t st) {
   if (M == 0) return cudaSuccess;
+  const bool vec = K % 8 == 0;
   switch (dt) {
-    case NF4_F32: return quantize_t<float>(x, M, K, out, status, st);
-    case NF4_BF16: return quantize_t<__nv_bfloat16>(x, M, K, out, status, st);
-    default: return quantize_t<__half>(x, M, K, out, status, st);
+    case NF4_F32:
+      return vec ? quantize_t<float, true>(x, M, K, out, status, st) : quantize_t<float, false>(x, M, K, out, status, st);
+    case NF4_BF16:
+      return vec ? quantize_t<__nv_bfloat16, true>(x, M, K, out, status, st)
+                 : quantize_t<__nv_bfloat16, false>(x, M, K, out, status, st);
+    default:
+      return vec ? quantize_t<__half, true>(x, M, K, out, status, st) : quantize_t<__half, false>(x, M, K, out, status, st);
   }
 }
 

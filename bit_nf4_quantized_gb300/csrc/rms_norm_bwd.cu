@@ -4,12 +4,14 @@
 //   dx = rstd (dn - n mean(dn n)) + dresidual,   dweight = sum over tokens of dy n
 //
 // One pass: a row's dn and n live in the registers of a group of threads between the sum and
-// the store.  CTAs walk over rows with a fixed set of columns for each thread, so dweight's
+// the store.  Groups walk over rows with a fixed set of columns for each thread, so dweight's
 // sums stay in registers too; each group writes them once and norm_dweight adds the groups in
-// a fixed order.  Bound by HBM: dy, dresidual, dx and h (or one byte a value) once each.
+// a fixed order.  Rows of whole 16-byte pieces come through a ring of bulk copies (row_ring.cuh);
+// others, and rows too long for the ring, are loaded by the threads themselves.  Bound by HBM: dy, dresidual, dx and h (or one byte a value) once each.
 #include <algorithm>
+#include <mutex>
 
-#include "train_ops.cuh"
+#include "row_ring.cuh"
 
 namespace qnf4 {
 namespace {
@@ -129,6 +131,116 @@ __global__ void __launch_bounds__(512) rms_norm_bwd(const NormBwdArgs a) {
   }
 }
 
+// Workers walk over rows: G threads a worker, blockDim.x / G workers a CTA.  kCk: n comes from the
+// checkpoint (K % 16 == 0: whole 16-byte pieces of codes), else from h.
+template <typename T, bool kCk, bool kDw>
+__global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, int G, int stages, int* status) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float red[2 * 32];
+  __shared__ uint64_t bars[kRingWarpWorkers * kRingStagesMax];
+  __shared__ int gave_up;
+  const int w = threadIdx.x / G, t = threadIdx.x - w * G;
+  const uint32_t row_bytes = static_cast<uint32_t>(a.K * sizeof(T));
+  const uint32_t saved_bytes = kCk ? static_cast<uint32_t>(a.K) : row_bytes;
+  const uint32_t bytes = row_bytes * (a.dresidual != nullptr ? 2 : 1) + saved_bytes;
+  uint8_t* ring = smem + static_cast<size_t>(w) * stages * bytes;
+  const uint32_t ring_at = tc::smem_u32(ring), bar_at = tc::smem_u32(bars + w * kRingStagesMax);
+  if (t == 0)
+    for (int s = 0; s < stages; ++s) tc::mbar_init(bar_at + 8 * s, 1);
+  if (threadIdx.x == 0) gave_up = 0;
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncthreads();
+  pdl_allow_next();
+  pdl_wait();
+  const int64_t workers = static_cast<int64_t>(gridDim.x) * (blockDim.x / G);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (blockDim.x / G) + w;
+  const int64_t nb = (a.K + kActBlock - 1) / kActBlock;
+  const int64_t blk = min(static_cast<int64_t>(t / (kActLanes / kRingN)), nb - 1);
+  const float invK = 1.0f / static_cast<float>(a.K);
+  auto issue = [&](int64_t m, int s) {
+    if (m >= a.M) return;
+    const uint32_t dst = ring_at + s * bytes, bar = bar_at + 8 * s;
+    tc::mbar_expect_tx(bar, bytes);
+    bulk_copy(dst, static_cast<const T*>(a.dy) + m * a.K, row_bytes, bar);
+    if (kCk) bulk_copy(dst + row_bytes, a.act.codes + m * a.K, saved_bytes, bar);
+    else bulk_copy(dst + row_bytes, static_cast<const T*>(a.h) + m * a.K, saved_bytes, bar);
+    if (a.dresidual != nullptr)
+      bulk_copy(dst + row_bytes + saved_bytes, static_cast<const T*>(a.dresidual) + m * a.K, row_bytes, bar);
+  };
+  if (t == 0)
+    for (int s = 0; s < stages; ++s) issue(first + s * workers, s);
+  float dw[kRingN][8];
+#pragma unroll
+  for (int u = 0; u < kRingN; ++u)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[u][j] = 0.0f;
+  // the row's rstd and the block's scale, one row ahead
+  float rstd_next = first < a.M ? a.rstd[first] : 0.0f;
+  float scale_next = kCk && first < a.M ? a.act.scales[first * nb + blk] : 0.0f;
+  int s = 0, turn = 0;
+  uint32_t ph = 0;
+  for (int64_t m = first; m < a.M; m += workers, turn ^= 1) {
+    const float rstd = rstd_next, scale = scale_next;
+    if (m + workers < a.M) {
+      rstd_next = a.rstd[m + workers];
+      if (kCk) scale_next = a.act.scales[(m + workers) * nb + blk];
+    }
+    tc::mbar_wait(bar_at + 8 * s, ph, &gave_up, status);   // see rms_norm_fwd_ring
+    const uint8_t* stage = ring + s * bytes;
+    float g[kRingN][8], n[kRingN][8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kRingN; ++u) {
+      const int64_t c = chunk_of(t, kRingN, u);
+      float wt[8];
+      load8<float, true>(a.weight, c, a.K, wt);
+      ring8<T>(stage, c, a.K, g[u]);
+      if (kCk) {
+        const uint2 q = load_codes<true>(reinterpret_cast<const int8_t*>(stage + row_bytes), c, a.K);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) n[u][j] = code_value(q, j) * scale;
+      } else {
+        ring8<T>(stage + row_bytes, c, a.K, n[u]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) n[u][j] *= rstd;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (kDw) dw[u][j] = fmaf(g[u][j], n[u][j], dw[u][j]);
+        g[u][j] *= wt[j];
+        sum = fmaf(g[u][j], n[u][j], sum);
+      }
+    }
+    const float mean = worker_sum(sum, G, red, turn) * invK;
+#pragma unroll
+    for (int u = 0; u < kRingN; ++u) {
+      const int64_t c = chunk_of(t, kRingN, u);
+      float o[8];
+      if (a.dresidual != nullptr) ring8<T>(stage + row_bytes + saved_bytes, c, a.K, o);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = rstd * (g[u][j] - n[u][j] * mean);
+        o[j] = a.dresidual != nullptr ? d + o[j] : d;
+      }
+      store8<T, true>(static_cast<T*>(a.dx) + m * a.K, c, a.K, o);
+    }
+    if (G == 32) __syncwarp();
+    else __syncthreads();
+    if (t == 0) issue(m + stages * workers, s);      // every thread has read the stage
+    if (++s == stages) s = 0, ph ^= 1u;
+  }
+  if (gave_up && t == 0)
+    for (int k = 0; k < stages; ++k) {
+      tc::mbar_drain(bar_at + 8 * s, ph);
+      if (++s == stages) s = 0, ph ^= 1u;
+    }
+  if (kDw) {
+    float* part = a.partial + first * a.K;
+#pragma unroll
+    for (int u = 0; u < kRingN; ++u) store8<float, true>(part, chunk_of(t, kRingN, u), a.K, dw[u]);
+  }
+}
+
 // dweight[k] = sum of the P groups' parts: 32 columns a CTA, 32 threads down the groups, then
 // their sums in order.
 __global__ void norm_dweight(const float* part, int64_t P, int64_t K, float* dweight) {
@@ -164,8 +276,43 @@ BwdShape bwd_shape(int64_t M, int64_t K) {
   return b;
 }
 
+// The ring's shape for a call, from what a row's inputs take (an element of `elem` bytes).
+RingShape bwd_ring(int64_t M, int64_t K, size_t elem, bool ck, bool dres) {
+  if (K % (ck ? 16 : 8) != 0) return RingShape{};
+  return ring_shape(M, K, K * elem * (dres ? 2 : 1) + K * (ck ? 1 : elem), 128);
+}
+
+template <typename T, bool kCk, bool kDw>
+cudaError_t launch_ring(const NormBwdArgs& a, const RingShape& r, int* status, cudaStream_t st) {
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [&] {
+    err = cudaFuncSetAttribute(rms_norm_bwd_ring<T, kCk, kDw>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(kRingSmemMax));
+  });
+  if (err != cudaSuccess) return err;
+  note_launch();
+  return launch_pdl(rms_norm_bwd_ring<T, kCk, kDw>, dim3(r.grid), dim3(r.G * r.workers), r.smem, st, 1, a, r.G, r.stages,
+                    status);
+}
+
+cudaError_t add_groups(const NormBwdArgs& a, int64_t groups, cudaStream_t st) {
+  note_launch();
+  return launch_pdl(norm_dweight, dim3(static_cast<unsigned>((a.K + kDwCols - 1) / kDwCols)), dim3(kDwCols, kDwRows), 0,
+                    st, 1, static_cast<const float*>(a.partial), groups, a.K, a.dweight);
+}
+
 template <typename T, bool kVec, bool kDw>
-cudaError_t launch(const NormBwdArgs& a, cudaStream_t st) {
+cudaError_t launch(const NormBwdArgs& a, int* status, cudaStream_t st) {
+  if (kVec) {
+    const bool ck = a.h == nullptr;
+    const RingShape r = bwd_ring(a.M, a.K, sizeof(T), ck, a.dresidual != nullptr);
+    if (r.stages > 0) {
+      const cudaError_t e = ck ? launch_ring<T, true, kDw>(a, r, status, st) : launch_ring<T, false, kDw>(a, r, status, st);
+      if (e != cudaSuccess || !kDw) return e;
+      return add_groups(a, std::min<int64_t>(static_cast<int64_t>(r.grid) * r.workers, a.M), st);
+    }
+  }
   const BwdShape b = bwd_shape(a.M, a.K);
   const dim3 grid(static_cast<unsigned>(b.grid)), block(b.row.G, b.row.R);
   cudaError_t e;
@@ -177,32 +324,38 @@ cudaError_t launch(const NormBwdArgs& a, cudaStream_t st) {
     default: e = launch_pdl(rms_norm_bwd<T, kVec, 0, kDw>, grid, block, 0, st, 1, a); break;
   }
   if (e != cudaSuccess || !kDw) return e;
-  note_launch();
-  return launch_pdl(norm_dweight, dim3(static_cast<unsigned>((a.K + kDwCols - 1) / kDwCols)), dim3(kDwCols, kDwRows), 0,
-                    st, 1, static_cast<const float*>(a.partial), static_cast<int64_t>(b.grid) * b.row.R, a.K, a.dweight);
+  return add_groups(a, static_cast<int64_t>(b.grid) * b.row.R, st);
 }
 
 template <typename T>
-cudaError_t pick(const NormBwdArgs& a, cudaStream_t st) {
+cudaError_t pick(const NormBwdArgs& a, int* status, cudaStream_t st) {
   const bool vec = a.K % 8 == 0;
-  if (a.dweight != nullptr) return vec ? launch<T, true, true>(a, st) : launch<T, false, true>(a, st);
-  return vec ? launch<T, true, false>(a, st) : launch<T, false, false>(a, st);
+  if (a.dweight != nullptr) return vec ? launch<T, true, true>(a, status, st) : launch<T, false, true>(a, status, st);
+  return vec ? launch<T, true, false>(a, status, st) : launch<T, false, false>(a, status, st);
 }
 
 }  // namespace
 
 size_t rms_norm_bwd_ws_bytes(int64_t M, int64_t K) {
   if (M == 0) return 0;
+  // the most groups any form of the call has: the ring's with the smallest rows, or the rows'
   const BwdShape b = bwd_shape(M, K);
-  return sizeof(float) * static_cast<size_t>(b.grid) * b.row.R * static_cast<size_t>(K);
+  int64_t groups = static_cast<int64_t>(b.grid) * b.row.R;
+  for (const size_t elem : {sizeof(float), sizeof(__half)})
+    for (const bool ck : {false, true})
+      for (const bool dres : {false, true}) {
+        const RingShape r = bwd_ring(M, K, elem, ck, dres);
+        if (r.stages > 0) groups = std::max<int64_t>(groups, static_cast<int64_t>(r.grid) * r.workers);
+      }
+  return sizeof(float) * static_cast<size_t>(groups) * static_cast<size_t>(K);
 }
 
-cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, nf4_dtype dt, cudaStream_t st) {
+cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, nf4_dtype dt, int* status, cudaStream_t st) {
   if (a.M == 0) return a.dweight != nullptr ? cudaMemsetAsync(a.dweight, 0, sizeof(float) * a.K, st) : cudaSuccess;
   switch (dt) {
-    case NF4_F32: return pick<float>(a, st);
-    case NF4_BF16: return pick<__nv_bfloat16>(a, st);
-    default: return pick<__half>(a, st);
+    case NF4_F32: return pick<float>(a, status, st);
+    case NF4_BF16: return pick<__nv_bfloat16>(a, status, st);
+    default: return pick<__half>(a, status, st);
   }
 }
 

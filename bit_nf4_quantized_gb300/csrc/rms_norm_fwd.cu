@@ -2,11 +2,15 @@
 //
 //   h = x + residual (fp32),  rstd = 1 / sqrt(mean h^2 + eps),  n = h rstd,  y = n weight
 //
-// One pass: a row lives in the registers of a group of threads (kNv chunks of 8 values each)
-// from its load to the stores of h, y and n's codes.  Bound by HBM: x, residual, h and y once
-// each, one byte a value and 4 / 128 for the checkpoint.  h is rounded when it is stored; the
-// norm is taken of the fp32 sum.
-#include "train_ops.cuh"
+// One pass: a row lives in the registers of a group of threads from its load to the stores of
+// h, y and n's codes.  Bound by HBM: x, residual, h and y once each, one byte a value and
+// 4 / 128 for the checkpoint.  h is rounded when it is stored; the norm is taken of the fp32
+// sum.  Rows of whole 16-byte pieces come through a ring of bulk copies (row_ring.cuh); others,
+// and rows too long for the ring, are loaded by the threads themselves.
+#include <algorithm>
+#include <mutex>
+
+#include "row_ring.cuh"
 
 namespace qnf4 {
 namespace {
@@ -32,26 +36,31 @@ __global__ void __launch_bounds__(512) rms_norm_fwd(const NormFwdArgs a, int* st
       for (int j = 0; j < 8; ++j) v[j] += r[j];
     }
   };
-  auto finish = [&](int64_t c, const float (&h)[8], float rstd) {
-    float n[8], y[8], w[8];
-    load8<float, kVec>(a.weight, c, a.K, w);
+  // the thread's kN chunks of one block, from h to the stores of h, y and the codes
+  auto finish = [&](int64_t t, auto& h, float rstd) {
+    constexpr int kN = sizeof(h) / (8 * sizeof(float));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) n[j] = h[j] * rstd, y[j] = n[j] * w[j];
-    if (on) store8<T, kVec>(static_cast<T*>(a.y) + at, c, a.K, y);
-    if (on && a.h != nullptr) store8<T, kVec>(static_cast<T*>(a.h) + at, c, a.K, h);
+    for (int u = 0; u < kN; ++u) {
+      const int64_t c = chunk_of(t, kN, u);
+      if (on && a.h != nullptr) store8<T, kVec>(static_cast<T*>(a.h) + at, c, a.K, h[u]);
+      float y[8], w[8];
+      load8<float, kVec>(a.weight, c, a.K, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[u][j] *= rstd, y[j] = h[u][j] * w[j];
+      if (on) store8<T, kVec>(static_cast<T*>(a.y) + at, c, a.K, y);
+    }
     if (a.act.codes != nullptr) {
-      const Quantized q = quantize_block(n);
-      if (on) store_codes<kVec>(a.act, m, c, a.K, q);
-      if (on && q.bad) atomicCAS(status, 0, static_cast<int>(NF4_ERR_NONFINITE));
+      const Quantized<kN> q = quantize_block<kN>(h);
+      if (on) store_block<kVec, kN>(a.act, m, t, a.K, q, status);
     }
   };
   float ss = 0.0f;
   if (kNv > 0) {
-    float h[kNv > 0 ? kNv : 1][8];
+    constexpr int kN = kNv > 0 ? kNv : 1;
+    float h[kN][8];
 #pragma unroll
-    for (int i = 0; i < kNv; ++i) {
-      const int64_t c = threadIdx.x + static_cast<int64_t>(i) * blockDim.x;
-      if (on) load(c, h[i]);
+    for (int i = 0; i < kN; ++i) {
+      if (on) load(chunk_of(threadIdx.x, kN, i), h[i]);
       else
         for (int j = 0; j < 8; ++j) h[i][j] = 0.0f;
 #pragma unroll
@@ -60,28 +69,125 @@ __global__ void __launch_bounds__(512) rms_norm_fwd(const NormFwdArgs a, int* st
     ss = group_sum(ss, red, 0);
     const float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.K) + a.eps);
     if (on && threadIdx.x == 0) a.rstd[m] = rstd;
-#pragma unroll
-    for (int i = 0; i < kNv; ++i) finish(threadIdx.x + static_cast<int64_t>(i) * blockDim.x, h[i], rstd);
+    finish(threadIdx.x, h, rstd);
   } else {
-    float h[8];
+    float h[1][8];
     for (int64_t c = threadIdx.x; c < C; c += blockDim.x) {   // one row a CTA: `on` holds
-      load(c, h);
+      load(c, h[0]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(h[j], h[j], ss);
+      for (int j = 0; j < 8; ++j) ss = fmaf(h[0][j], h[0][j], ss);
     }
     ss = group_sum(ss, red, 0);
     const float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.K) + a.eps);
     if (threadIdx.x == 0) a.rstd[m] = rstd;
     // every lane of a warp runs the same rounds: the quantizer shuffles
     for (int64_t c0 = 0; c0 < C; c0 += blockDim.x) {
-      load(c0 + threadIdx.x, h);
+      load(c0 + threadIdx.x, h[0]);
       finish(c0 + threadIdx.x, h, rstd);
     }
   }
 }
 
+// Workers walk over rows: G threads a worker, blockDim.x / G workers a CTA.
+template <typename T>
+__global__ void __launch_bounds__(512) rms_norm_fwd_ring(const NormFwdArgs a, int G, int stages, int* status) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float red[2 * 32];
+  __shared__ uint64_t bars[kRingWarpWorkers * kRingStagesMax];
+  __shared__ int gave_up;
+  const int w = threadIdx.x / G, t = threadIdx.x - w * G;
+  const uint32_t row_bytes = static_cast<uint32_t>(a.K * sizeof(T));
+  const uint32_t bytes = row_bytes * (a.residual != nullptr ? 2 : 1);
+  uint8_t* ring = smem + static_cast<size_t>(w) * stages * bytes;
+  const uint32_t ring_at = tc::smem_u32(ring), bar_at = tc::smem_u32(bars + w * kRingStagesMax);
+  if (t == 0)
+    for (int s = 0; s < stages; ++s) tc::mbar_init(bar_at + 8 * s, 1);
+  if (threadIdx.x == 0) gave_up = 0;
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncthreads();
+  pdl_allow_next();
+  pdl_wait();
+  const int64_t workers = static_cast<int64_t>(gridDim.x) * (blockDim.x / G);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (blockDim.x / G) + w;
+  auto issue = [&](int64_t m, int s) {
+    if (m >= a.M) return;
+    tc::mbar_expect_tx(bar_at + 8 * s, bytes);
+    bulk_copy(ring_at + s * bytes, static_cast<const T*>(a.x) + m * a.K, row_bytes, bar_at + 8 * s);
+    if (a.residual != nullptr)
+      bulk_copy(ring_at + s * bytes + row_bytes, static_cast<const T*>(a.residual) + m * a.K, row_bytes, bar_at + 8 * s);
+  };
+  if (t == 0)
+    for (int s = 0; s < stages; ++s) issue(first + s * workers, s);
+  float wt[kRingN][8];      // the thread's columns are the same for every row
+#pragma unroll
+  for (int u = 0; u < kRingN; ++u) load8<float, true>(a.weight, chunk_of(t, kRingN, u), a.K, wt[u]);
+  int s = 0, turn = 0;
+  uint32_t ph = 0;
+  for (int64_t m = first; m < a.M; m += workers, turn ^= 1) {
+    // a wait that gives up leaves the loop's shape as it is: the later ones return at once
+    tc::mbar_wait(bar_at + 8 * s, ph, &gave_up, status);
+    const uint8_t* stage = ring + s * bytes;
+    float h[kRingN][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kRingN; ++u) {
+      const int64_t c = chunk_of(t, kRingN, u);
+      ring8<T>(stage, c, a.K, h[u]);
+      if (a.residual != nullptr) {
+        float r[8];
+        ring8<T>(stage + row_bytes, c, a.K, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[u][j] += r[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(h[u][j], h[u][j], ss);
+    }
+    ss = worker_sum(ss, G, red, turn);
+    if (t == 0) issue(m + stages * workers, s);      // every thread has read the stage
+    const float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.K) + a.eps);
+    if (t == 0) a.rstd[m] = rstd;
+    const int64_t at = m * a.K;
+#pragma unroll
+    for (int u = 0; u < kRingN; ++u) {
+      const int64_t c = chunk_of(t, kRingN, u);
+      if (a.h != nullptr) store8<T, true>(static_cast<T*>(a.h) + at, c, a.K, h[u]);
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[u][j] *= rstd, y[j] = h[u][j] * wt[u][j];
+      store8<T, true>(static_cast<T*>(a.y) + at, c, a.K, y);
+    }
+    if (a.act.codes != nullptr) {
+      const Quantized<kRingN> q = quantize_block<kRingN>(h);
+      store_block<true, kRingN>(a.act, m, t, a.K, q, status);
+    }
+    if (++s == stages) s = 0, ph ^= 1u;
+  }
+  if (gave_up && t == 0)
+    for (int k = 0; k < stages; ++k) {   // let copies in flight land before the CTA exits
+      tc::mbar_drain(bar_at + 8 * s, ph);
+      if (++s == stages) s = 0, ph ^= 1u;
+    }
+}
+
+template <typename T>
+cudaError_t launch_ring(const NormFwdArgs& a, const RingShape& r, int* status, cudaStream_t st) {
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [&] {
+    err = cudaFuncSetAttribute(rms_norm_fwd_ring<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(kRingSmemMax));
+  });
+  if (err != cudaSuccess) return err;
+  note_launch();
+  return launch_pdl(rms_norm_fwd_ring<T>, dim3(r.grid), dim3(r.G * r.workers), r.smem, st, 1, a, r.G, r.stages, status);
+}
+
 template <typename T, bool kVec>
 cudaError_t launch(const NormFwdArgs& a, int* status, cudaStream_t st) {
+  if (kVec) {
+    const RingShape r = ring_shape(a.M, a.K, a.K * sizeof(T) * (a.residual != nullptr ? 2 : 1), 128);
+    if (r.stages > 0) return launch_ring<T>(a, r, status, st);
+  }
   const int64_t C = (a.K + kActBlock - 1) / kActBlock * kActLanes;
   const int nv = C <= 512 ? 1 : C <= 1024 ? 2 : C <= 2048 ? 4 : 0;
   const RowShape s = nv > 0 ? row_shape(C, nv) : RowShape{512, 1};

@@ -7,10 +7,11 @@
 // (127 / amax could overflow) is stored as zeros.  A block holding a NaN or an infinity gets
 // the scale NaN, so that everything read from it is NaN, and sets NF4_ERR_NONFINITE.
 //
-// Layout shared by the kernels: the 128 features of a block belong to 16 neighbouring lanes,
-// 8 values each.  With K % 8 == 0 every row is 16-byte aligned and a lane's 8 values are
-// contiguous (kVec: 16-byte accesses); otherwise lane i takes features i, i + 16, ... of its
-// block, so that the 16 lanes' narrow accesses stay within the same sectors.
+// Layout shared by the kernels: a row is cut in chunks of 8 values, 16 chunks a block.  With
+// K % 8 == 0 every row is 16-byte aligned and a chunk is contiguous (kVec: 16-byte accesses);
+// otherwise chunk i of a block takes features i, i + 16, ... of it, so that neighbouring lanes'
+// narrow accesses stay within the same sectors.  A thread may hold n = 1, 2 or 4 chunks of one
+// block, 16 / n lanes then sharing it (chunk_of): the block's scale costs two divisions a lane.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -55,7 +56,7 @@ struct NormBwdArgs {
   float* partial;         // rms_norm_bwd_ws_bytes, with dweight
 };
 size_t rms_norm_bwd_ws_bytes(int64_t M, int64_t K);
-cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, nf4_dtype dt, cudaStream_t st);
+cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, nf4_dtype dt, int* status, cudaStream_t st);
 
 // ---- act8.cu ------------------------------------------------------------------------------
 cudaError_t launch_act8_quantize(const void* x, nf4_dtype dt, int64_t M, int64_t K, Act8View out, int* status,
@@ -162,56 +163,78 @@ __device__ __forceinline__ float code_value(uint2 q, int j) {
   return __uint_as_float(f) - 8388736.0f;
 }
 
-// Quantizes the 16 lanes' block: every lane of the warp calls it.  Returns the codes of this
-// lane's values and the block's scale.
+// Chunk u of thread t's n: lanes t % (16 / n) + (16 / n) u of block t / (16 / n).
+__device__ __forceinline__ int64_t chunk_of(int64_t t, int n, int u) {
+  const int lanes = kActLanes / n;
+  return t / lanes * kActLanes + t % lanes + lanes * u;
+}
+
+__device__ __forceinline__ float max_abs_nan(float a, float b) {   // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
+// Quantizes a block held by 16 / kN neighbouring lanes, kN chunks each; every lane of the warp
+// calls it.  Codes are rint(v * inv) by way of 1.5 * 2^23: the product is rounded to fp32, then
+// the sum's last byte is the code in two's complement.
+template <int kN>
 struct Quantized {
-  uint2 codes;
+  uint2 codes[kN];
   float scale;
   bool bad;
 };
-__device__ __forceinline__ Quantized quantize_block(const float (&v)[8]) {
+template <int kN>
+__device__ __forceinline__ Quantized<kN> quantize_block(const float (&v)[kN][8]) {
   float amax = 0.0f;
-  bool bad = false;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float a = fabsf(v[j]);
-    bad |= !(a < INFINITY);
-    amax = fmaxf(amax, a);
-  }
+  for (int u = 0; u < kN; ++u)
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    bad |= __shfl_xor_sync(0xffffffffu, static_cast<int>(bad), o) != 0;
-  }
-  Quantized q;
-  q.bad = bad;
-  const bool live = amax >= kActTiny && !bad;
+    for (int j = 0; j < 8; ++j) amax = max_abs_nan(amax, v[u][j]);
+#pragma unroll
+  for (int o = kActLanes / kN / 2; o > 0; o >>= 1) amax = max_abs_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  Quantized<kN> q;
+  q.bad = !(amax < INFINITY);
+  const bool live = amax >= kActTiny && !q.bad;
   const float inv = live ? 127.0f / amax : 0.0f;
-  q.scale = bad ? __int_as_float(0x7fc00000) : live ? amax / 127.0f : 0.0f;
-  uint32_t w[2] = {0, 0};
-  if (!bad) {
+  q.scale = q.bad ? __int_as_float(0x7fc00000) : live ? amax / 127.0f : 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      w[j / 4] |= (static_cast<uint32_t>(__float2int_rn(v[j] * inv)) & 0xffu) << (8 * (j & 3));
+  for (int u = 0; u < kN; ++u) {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[u][j], inv), 12582912.0f));
+    q.codes[u].x = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+    q.codes[u].y = __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410);
+    if (q.bad) q.codes[u] = make_uint2(0, 0);
   }
-  q.codes = make_uint2(w[0], w[1]);
   return q;
 }
 
-// Stores a lane's codes, and the scale from the block's first lane.
+// Stores chunk c's codes.
 template <bool kVec>
-__device__ __forceinline__ void store_codes(const Act8View& a, int64_t m, int64_t c, int64_t K, const Quantized& q) {
-  if ((c / kActLanes) * kActBlock >= K) return;
-  int8_t* row = a.codes + m * K;
+__device__ __forceinline__ void store_codes(int8_t* row, int64_t c, int64_t K, uint2 q) {
   if (kVec) {
-    if (c * 8 < K) *reinterpret_cast<uint2*>(row + c * 8) = q.codes;
+    if (c * 8 < K) *reinterpret_cast<uint2*>(row + c * 8) = q;
   } else {
     const int64_t e = (c / kActLanes) * kActBlock + c % kActLanes;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (e + 16 * j < K) row[e + 16 * j] = static_cast<int8_t>((j < 4 ? q.codes.x : q.codes.y) >> (8 * (j & 3)));
+      if (e + 16 * j < K) row[e + 16 * j] = static_cast<int8_t>((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
   }
-  if (c % kActLanes == 0) a.scales[m * ((K + kActBlock - 1) / kActBlock) + c / kActLanes] = q.scale;
+}
+
+// Stores what a thread quantized: its chunks' codes, and the scale from the block's first lane.
+template <bool kVec, int kN>
+__device__ __forceinline__ void store_block(const Act8View& a, int64_t m, int64_t t, int64_t K, const Quantized<kN>& q,
+                                            int* status) {
+  const int64_t b = t / (kActLanes / kN);
+  if (b * kActBlock >= K) return;
+#pragma unroll
+  for (int u = 0; u < kN; ++u) store_codes<kVec>(a.codes + m * K, chunk_of(t, kN, u), K, q.codes[u]);
+  if (t % (kActLanes / kN) == 0) {
+    a.scales[m * ((K + kActBlock - 1) / kActBlock) + b] = q.scale;
+    if (q.bad) atomicCAS(status, 0, static_cast<int>(NF4_ERR_NONFINITE));
+  }
 }
 
 // Sum over a row's group of threads (threadIdx.x of a (G, R) block, G a multiple of 32);
