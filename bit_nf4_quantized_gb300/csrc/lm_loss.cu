@@ -11,26 +11,28 @@
 // would take 6 M V D.  The target's own term stays out of P: near a sure token
 // 1 - own / (others + own) cancels, others / (others + own) does not.
 //
-// R starts as the target's logit (for half, whose largest value is 65504, the larger of it and
-// of the logits of the vocabulary's first 256 tokens).  Only range matters: a bf16 P holds
-// exp(z - R) up to z - R = 88, a half one up to 11.  A logit further above R than that is found
-// by the pass that meets it, which records the row's largest; the token tiles with such a row
-// run that piece once more with the raised R, and the sums taken so far are scaled by
-// exp(R_old - R_new).  R never exceeds the largest logit, so the largest term never vanishes.
+// R starts as the target's logit (for half, whose largest value is 65504, the largest of it and
+// of 8 other entries' logits).  Only range matters: a bf16 P holds exp(z - R) up to z - R = 88,
+// a half one up to 11.  A logit further above R than that is found by the pass that meets it,
+// which records the row's largest; the token tiles with such a row run that piece once more with
+// the raised R, and the sums taken so far are scaled by exp(R_old - R_new).  R never exceeds the
+// largest logit, so the largest term never vanishes.  Exponentials are powers of two of
+// z log2(e) - R2 with R2 the reference in those units: the rounding of R2 is common to every
+// term and cancels.
 //
 // Kernels.
-//   lm_target     z[t][y], the tokens that count, R's start
+//   lm_prep       z[t][y], the tokens that count, R's start
 //   lm_gemm<kScores / kMax>  clusters of two CTAs, persistent over tiles of 256 tokens x 256
 //                 vocabulary entries: 2-SM tcgen05.mma with x as A (each token's logits in one
 //                 TMEM lane, so a thread owns a row), W as B, both K-major through TMA.  The
 //                 epilogue takes exponentials, row sums and P (bf16 / half through a swizzled
-//                 shared-memory box and a TMA store), or, without a gradient, each tile's row
-//                 maximum and sum.
+//                 shared-memory box and a TMA store), or, without a gradient, each half tile's
+//                 row maximum and sum.
 //   lm_gemm<kGrad>   tiles of 256 features x 256 tokens: A = W[piece] read MN-major, B = P;
 //                 the contraction (the piece) is split in `slices` parts with an fp32 sum each
 //                 when there are too few tiles for the SMs.
-//   lm_rows       each token's totals, loss, lse and the two factors of dx
-//   lm_dx         dx = a (sum of the slices) - b W[y], rounded once to 16 bits
+//   lm_finish     each token's totals, loss and lse, and dx = a (sum of the slices) - b W[y],
+//                 rounded once to 16 bits
 //
 // Roundings to 16 bits: P (a relative 2^-9 of each term of the sum, the target's excepted)
 // and dx itself; logits, exponentials, sums and statistics are fp32.
@@ -59,19 +61,25 @@ constexpr int kSubBytes = kHalf * kSub * 2; // 16 KB: 128 rows of A, or the CTA'
 constexpr int kHalfSub = kSubBytes / 2;     // one 64-feature half of an MN-major sub-block
 constexpr int kStageBytes = 2 * kSubs * kSubBytes;
 constexpr int kStages = 3;
-constexpr int kThreads = 192;               // TMA warp, MMA warp, 4 epilogue warps
+// TMA warp, MMA warp, 8 epilogue warps: two for each 32 TMEM lanes, half of the columns each
+// (with 4 warps the epilogue of a 576-deep tile took longer than its products)
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kEpiCols = kTile / 2;
 constexpr int kTmemCols = 512;
-constexpr int kBoxBytes = 32 * 128;         // a warp's store box: 32 tokens x 64 values
+constexpr int kBoxCols = 32;                // a warp's store box: 32 tokens x 32 values
+constexpr int kBoxBytes = 32 * kBoxCols * 2;
 constexpr int kBoxes = 2;                   // per epilogue warp
 constexpr int kBarFull = 0, kBarEmpty = kStages, kBarAccFull = 2 * kStages, kBarAccEmpty = kBarAccFull + 2,
               kBarDone = kBarAccEmpty + 2, kNumBars = kBarDone + 1;
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 4 * kBoxes * kBoxBytes + kNumBars * 8 + 16;
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiWarps * kBoxes * kBoxBytes + kNumBars * 8 + 16;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
-constexpr float kLog2e = 1.4426950408889634f;
-// how far above R a logit may lie: exp(60) leaves the fp32 sums of any vocabulary finite;
-// exp(11) is the largest integer power below half's 65504
-constexpr float kRangeBf16 = 60.0f, kRangeF16 = 11.0f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// how far above R a logit may lie, as powers of two: 2^86 leaves the fp32 sums of any vocabulary
+// finite; 2^15.9 is below half's 65504
+constexpr float kRangeBf16 = 86.0f, kRangeF16 = 15.9f;
+constexpr int kSamples = 8;                 // entries whose logits half's R starts from, beside the target
 
 enum { kScores = 0, kMax = 1, kGrad = 2 };
 
@@ -90,12 +98,12 @@ struct LmParams {
   int add;              // kGrad: add to the sums of the pieces before
   float range;
   const int64_t* targets;   // clean: the target, or -1 for a token that does not count
-  const float* ref;         // [M] R for this piece
+  const float* ref;         // [M] R for this piece, times log2(e)
   float* ref_next;          // [M] redo: R after this piece
   float* spike;             // [M] largest logit beyond the range in this piece, or -inf
   int* flags;               // [tiles_t] a row of the tile went beyond the range
-  float* part_sum;          // [vocabulary tile][M]
-  float* part_max;          // kMax: [vocabulary tile][M]
+  float* part_sum;          // [half vocabulary tile][M]
+  float* part_max;          // kMax: [half vocabulary tile][M], times log2(e)
   float* acc;               // kGrad: [slices][M][D]
   int* status;
   uint64_t wait_ns;
@@ -111,26 +119,26 @@ struct Ring {
 };
 
 struct Unit {
-  int64_t t, f;         // token tile; vocabulary or feature tile
-  int64_t k0;           // first contraction element
+  int t, f;             // token tile; vocabulary or feature tile
+  int k0;               // first contraction element
   int nsub;             // 64-deep sub-blocks
   int slice;
 };
 
 template <int MODE>
-__device__ __forceinline__ Unit unit_of(const LmParams& p, int64_t u) {
+__device__ __forceinline__ Unit unit_of(const LmParams& p, int u) {
   Unit x;
   x.slice = 0;
   if (MODE == kGrad) {
-    const int64_t tiles = static_cast<int64_t>(p.tiles_t) * p.tiles_f;
-    x.slice = static_cast<int>(u / tiles);
+    const int tiles = p.tiles_t * p.tiles_f;
+    x.slice = u / tiles;
     u -= x.slice * tiles;
   }
   if (MODE == kGrad && p.band > 0) {
-    const int64_t per = static_cast<int64_t>(p.band) * p.tiles_f;
-    const int64_t bi = u / per, t0 = bi * p.band;
-    const int64_t bt = min(static_cast<int64_t>(p.band), static_cast<int64_t>(p.tiles_t) - t0);
-    const int64_t idx = u - bi * per;
+    const int per = p.band * p.tiles_f;
+    const int bi = u / per, t0 = bi * p.band;
+    const int bt = min(p.band, p.tiles_t - t0);
+    const int idx = u - bi * per;
     x.t = t0 + idx % bt;
     x.f = idx / bt;
   } else {
@@ -142,9 +150,9 @@ __device__ __forceinline__ Unit unit_of(const LmParams& p, int64_t u) {
     s0 = static_cast<int>(static_cast<int64_t>(p.red_steps) * x.slice / p.slices);
     s1 = static_cast<int>(static_cast<int64_t>(p.red_steps) * (x.slice + 1) / p.slices);
   }
-  x.k0 = static_cast<int64_t>(s0) * kStepK;
-  const int64_t len = min(p.red_len, static_cast<int64_t>(s1) * kStepK) - x.k0;
-  x.nsub = static_cast<int>((len + kSub - 1) / kSub);
+  x.k0 = s0 * kStepK;
+  const int len = min(static_cast<int>(p.red_len), s1 * kStepK) - x.k0;
+  x.nsub = (len + kSub - 1) / kSub;
   return x;
 }
 
@@ -190,7 +198,7 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* base_ptr = smem_raw + (base - raw);
   const uint32_t boxes = base + kStages * kStageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base_ptr + kStages * kStageBytes + 4 * kBoxes * kBoxBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base_ptr + kStages * kStageBytes + kEpiWarps * kBoxes * kBoxBytes);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kNumBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars) + 1;
   auto bar = [&](int i) { return smem_u32(bars + i); };
@@ -198,12 +206,23 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
   auto stage_b = [&](int s) { return base + s * kStageBytes + kSubs * kSubBytes; };
   const uint32_t rank = cluster_ctarank();
   auto lead_bar = [&](int i) { return mapa_shared(bar(i), 0); };
-  const int64_t cluster_id = blockIdx.x / kCluster;
-  const int64_t n_clusters = gridDim.x / kCluster;
-  const int64_t total = static_cast<int64_t>(p.tiles_t) * p.tiles_f * (MODE == kGrad ? p.slices : 1);
+  const int cluster_id = blockIdx.x / kCluster;
+  const int n_clusters = gridDim.x / kCluster;
+  const int total = p.tiles_t * p.tiles_f * (MODE == kGrad ? p.slices : 1);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  if (MODE == kScores && p.redo) {
+    // a repeated pass raises R; without a flag it does nothing else
+    pdl_allow_next();
+    pdl_wait();
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; t < p.M;
+         t += static_cast<int64_t>(gridDim.x) * kThreads)
+      p.ref_next[t] = fmaxf(p.ref[t], p.spike[t]);
+    bool any = false;
+    for (int i = lane; i < p.tiles_t; i += 32) any |= p.flags[i] != 0;
+    if (!__any_sync(0xffffffffu, any)) return;
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(kBarFull + s), 1);
@@ -211,7 +230,7 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar(kBarAccFull + b), 1);
-      mbar_init(bar(kBarAccEmpty + b), 4 * kCluster);
+      mbar_init(bar(kBarAccEmpty + b), kEpiWarps * kCluster);
     }
     mbar_init(bar(kBarDone), 1);
     *abort_flag = 0;
@@ -220,11 +239,6 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
   pdl_allow_next();
   // TMEM is taken only after the preceding grid has completed (see linear_tc.cu)
   pdl_wait();
-  if (MODE == kScores && p.redo) {
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; t < p.M;
-         t += static_cast<int64_t>(gridDim.x) * kThreads)
-      p.ref_next[t] = fmaxf(p.ref[t], p.spike[t]);
-  }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(kTmemCols)
@@ -246,7 +260,7 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
       Ring c;
       int64_t issued = 0;
       int64_t lt = 0;
-      for (int64_t u = cluster_id; ok && u < total; u += n_clusters) {
+      for (int u = cluster_id; ok && u < total; u += n_clusters) {
         const Unit un = unit_of<MODE>(p, u);
         if (!runs(un)) continue;
         // A rows / B rows of this CTA, as tensor coordinates
@@ -305,7 +319,7 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
       bool ok = true;
       Ring c;
       int64_t lt = 0;
-      for (int64_t u = cluster_id; ok && u < total; u += n_clusters) {
+      for (int u = cluster_id; ok && u < total; u += n_clusters) {
         const Unit un = unit_of<MODE>(p, u);
         if (!runs(un)) continue;
         const int nsteps = (un.nsub + kSubs - 1) / kSubs;
@@ -343,13 +357,14 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
       mbar_drain(bar(kBarDone), 0);
     }
   } else {
-    // ---------------- epilogue: each warp on its own 32 TMEM lanes ----------------
+    // ---------------- epilogue: each warp on 32 TMEM lanes and half of the columns ----------------
     const int quarter = warp & 3;
     const int lrow = quarter * 32 + lane;
-    const uint32_t my_box = boxes + static_cast<uint32_t>(quarter * kBoxes * kBoxBytes);
+    const int half = (warp - 2) >> 2, cb = half * kEpiCols, ce = cb + kEpiCols;
+    const uint32_t my_box = boxes + static_cast<uint32_t>((warp - 2) * kBoxes * kBoxBytes);
     uint32_t nst = 0;
     int64_t lt = 0;
-    for (int64_t u = cluster_id; u < total; u += n_clusters) {
+    for (int u = cluster_id; u < total; u += n_clusters) {
       const Unit un = unit_of<MODE>(p, u);
       if (!runs(un)) continue;
       const uint32_t b = static_cast<uint32_t>(lt) & 1u;
@@ -359,12 +374,12 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
       const uint32_t taddr = tmem_base + b * kTile + (static_cast<uint32_t>(quarter * 32) << 16);
       if (MODE == kGrad) {
         // lane: one feature; columns: tokens.  Sums of the pieces before are in units of
-        // exp(-ref); this piece's in exp(-ref_next)
-        const int64_t f = un.f * kTile + static_cast<int64_t>(rank) * kHalf + lrow;
+        // 2^-ref; this piece's in 2^-ref_next
+        const int64_t f = static_cast<int64_t>(un.f) * kTile + static_cast<int64_t>(rank) * kHalf + lrow;
         float* dst = p.acc + static_cast<int64_t>(un.slice) * p.M * p.D + f;
-        const int64_t t0 = un.t * kTile;
+        const int64_t t0 = static_cast<int64_t>(un.t) * kTile;
 #pragma unroll 1
-        for (int c0 = 0; c0 < kTile && t0 + c0 < p.M; c0 += 16) {
+        for (int c0 = cb; c0 < ce && t0 + c0 < p.M; c0 += 16) {
           uint32_t v[16];
           tmem_ld16(taddr + c0, v);
           float old[16];
@@ -374,7 +389,7 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
               const int64_t t = t0 + c0 + j;
               old[j] = (t < p.M && f < p.D) ? dst[t * p.D] : 0.0f;
               const float r0 = t < p.M ? p.ref[t] : 0.0f, r1 = t < p.M ? p.ref_next[t] : 0.0f;
-              if (r0 != r1) old[j] *= __expf(r0 - r1);
+              if (r0 != r1) old[j] *= exp2f(r0 - r1);
             }
           }
           tmem_ld_wait();
@@ -388,15 +403,16 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
         }
       } else {
         // lane: one token; columns: vocabulary entries
-        const int64_t t0w = un.t * kTile + static_cast<int64_t>(rank) * kHalf + quarter * 32;
+        const int64_t t0w = static_cast<int64_t>(un.t) * kTile + static_cast<int64_t>(rank) * kHalf + quarter * 32;
         const int64_t t = t0w + lane;
-        const int64_t c_tile = un.f * kTile;                         // first column within the piece
+        const int64_t c_tile = static_cast<int64_t>(un.f) * kTile;   // first column within the piece
         const int64_t y = t < p.M ? p.targets[t] : -1;
         const bool live = y >= 0;
         const int64_t yc64 = y - p.v0 - c_tile;
-        const int yc = (live && yc64 >= 0 && yc64 < kTile) ? static_cast<int>(yc64) : -1;
+        const int yc = (live && yc64 >= cb && yc64 < ce) ? static_cast<int>(yc64) : -1;
         const int valid = static_cast<int>(min(static_cast<int64_t>(kTile), p.cols - c_tile));
-        const bool masked = __any_sync(0xffffffffu, yc >= 0) || valid < kTile;
+        const bool masked = __any_sync(0xffffffffu, yc >= 0) || valid < ce;
+        const int64_t part = (static_cast<int64_t>(un.f) * 2 + half) * p.M + t;
         auto mask = [&](uint32_t (&v)[32], int c0) {
           if (masked) {
 #pragma unroll
@@ -407,7 +423,7 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
         if (MODE == kMax) {
           float mx = -INFINITY;
 #pragma unroll 1
-          for (int c0 = 0; c0 < kTile; c0 += 32) {
+          for (int c0 = cb; c0 < ce; c0 += 32) {
             uint32_t v[32];
             tmem_ld32(taddr + c0, v);
             tmem_ld_wait();
@@ -418,7 +434,7 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
           const float m2 = mx == -INFINITY ? 0.0f : mx * kLog2e;
           float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-          for (int c0 = 0; c0 < kTile; c0 += 32) {
+          for (int c0 = cb; c0 < ce; c0 += 32) {
             uint32_t v[32];
             tmem_ld32(taddr + c0, v);
             tmem_ld_wait();
@@ -427,58 +443,56 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
             for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(__uint_as_float(v[j]), kLog2e, -m2));
           }
           if (t < p.M) {
-            p.part_max[un.f * p.M + t] = mx;
-            p.part_sum[un.f * p.M + t] = (s[0] + s[1]) + (s[2] + s[3]);
+            p.part_max[part] = mx == -INFINITY ? mx : m2;
+            p.part_sum[part] = (s[0] + s[1]) + (s[2] + s[3]);
           }
         } else {
-          float ref = t < p.M ? p.ref[t] : 0.0f;
-          if (p.redo && t < p.M) ref = fmaxf(ref, p.spike[t]);
-          const float r2 = ref * kLog2e;
+          float r2 = t < p.M ? p.ref[t] : 0.0f;
+          if (p.redo && t < p.M) r2 = fmaxf(r2, p.spike[t]);
           const uint32_t keep = live ? 0xffffffffu : 0u;
           float mx = -INFINITY;
           float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-          for (int c0 = 0; c0 < kTile; c0 += 64, ++nst) {
+          for (int c0 = cb; c0 < ce; c0 += kBoxCols, ++nst) {
             const uint32_t box = my_box + (nst & 1u) * kBoxBytes;
+            uint32_t v[32];
+            tmem_ld32(taddr + c0, v);
             if (lane == 0) bulk_wait_read<1>();      // the store that last used this box has read it
             __syncwarp();
+            tmem_ld_wait();
+            mask(v, c0);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t v[32];
-              tmem_ld32(taddr + c0 + h * 32, v);
-              tmem_ld_wait();
-              mask(v, c0 + h * 32);
+            for (int j = 0; j < 32; j += 8) {
+              uint32_t o[4];
 #pragma unroll
-              for (int j = 0; j < 32; j += 8) {
-                uint32_t o[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float z0 = __uint_as_float(v[j + 2 * k]), z1 = __uint_as_float(v[j + 2 * k + 1]);
-                  mx = fmaxf(mx, fmaxf(z0, z1));
-                  const float e0 = ex2(fmaf(z0, kLog2e, -r2)), e1 = ex2(fmaf(z1, kLog2e, -r2));
-                  s[k] += e0;
-                  s[k] += e1;
-                  o[k] = pack2(e0, e1, p.f16) & keep;
-                }
-                // row `lane` of the box, 16-byte column h * 4 + j / 8, 128-byte swizzle
-                const uint32_t col = static_cast<uint32_t>(h * 4 + j / 8) ^ (static_cast<uint32_t>(lane) & 7u);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 128 + col * 16), "r"(o[0]),
-                             "r"(o[1]), "r"(o[2]), "r"(o[3])
-                             : "memory");
+              for (int k = 0; k < 4; ++k) {
+                const float z0 = __uint_as_float(v[j + 2 * k]), z1 = __uint_as_float(v[j + 2 * k + 1]);
+                mx = fmaxf(mx, fmaxf(z0, z1));
+                const float e0 = ex2(fmaf(z0, kLog2e, -r2)), e1 = ex2(fmaf(z1, kLog2e, -r2));
+                s[k] += e0;
+                s[k] += e1;
+                o[k] = pack2(e0, e1, p.f16) & keep;
               }
+              // row `lane` of the box, 16-byte column j / 8, 64-byte swizzle
+              const uint32_t col = static_cast<uint32_t>(j / 8) ^ ((static_cast<uint32_t>(lane) >> 1) & 3u);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * (kBoxCols * 2) + col * 16),
+                           "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                           : "memory");
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
-              // columns past the piece hold zeros up to the next 64
-              if (t0w < p.M && c0 < valid) tma_store_2d(&tm_p, box, static_cast<int>(c_tile) + c0, static_cast<int>(t0w));
+              // the contraction over P goes on in zeros up to the next 64 columns
+              if (t0w < p.M && c0 < (valid + kSub - 1) / kSub * kSub)
+                tma_store_2d(&tm_p, box, static_cast<int>(c_tile) + c0, static_cast<int>(t0w));
               bulk_commit();
             }
           }
           if (t < p.M) {
-            p.part_sum[un.f * p.M + t] = live ? (s[0] + s[1]) + (s[2] + s[3]) : 0.0f;
-            if (live && !p.redo && mx > ref + p.range) {
-              atomic_max_float(p.spike + t, mx);
+            p.part_sum[part] = live ? (s[0] + s[1]) + (s[2] + s[3]) : 0.0f;
+            const float m2 = mx * kLog2e;
+            if (live && !p.redo && m2 > r2 + p.range) {
+              atomic_max_float(p.spike + t, m2);
               p.flags[un.t] = 1;
             }
           }
@@ -514,25 +528,17 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// A clean copy of the targets (-1: the token does not count), and the rows of a stored head to
-// decode (0 for those).  A target outside [0, V) that is not ignore_index sets NF4_ERR_ARG.
-__global__ void lm_clean(const int64_t* targets, int64_t M, int64_t V, int64_t ignore, int64_t* clean, int64_t* ids,
-                         int* status) {
-  pdl_allow_next();
-  pdl_wait();
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (t >= M) return;
-  const int64_t y = targets[t];
-  const bool in = y >= 0 && y < V && y != ignore;
-  if (!in && y != ignore) atomicCAS(status, 0, static_cast<int>(NF4_ERR_ARG));
-  clean[t] = in ? y : -1;
-  ids[t] = in ? y : 0;
+// The target of a token, or -1 where it does not count.
+__device__ __forceinline__ int64_t clean_target(int64_t y, int64_t V, int64_t ignore) {
+  return y >= 0 && y < V && y != ignore ? y : -1;
 }
+// Entry i of the kSamples of a vocabulary.
+__device__ __forceinline__ int64_t sample_of(int i, int64_t V) { return V * i / kSamples; }
 
-// The targets' rows of a stored head: out[t][d..d+7] = T16(nf4[code] * a') of row ids[t], the
-// bits nf4_dequantize writes.
-__global__ void lm_stored_rows(const Nf4View W, const DecodeTables tabs, const int64_t* ids, int64_t M, int64_t D8,
-                               int f16, uint4* out) {
+// Rows of a stored head: out[t][d..d+7] = T16(nf4[code] * a'), the bits nf4_dequantize writes, of
+// the targets' rows (0 for a token that does not count) and then of the samples'.
+__global__ void lm_stored_rows(const Nf4View W, const DecodeTables tabs, const int64_t* targets, int64_t M, int64_t V,
+                               int64_t ignore, int64_t D8, int f16, uint4* out) {
   __shared__ float dyn8[256];
   __shared__ float nf4[16];
   for (int i = threadIdx.x; i < 256; i += blockDim.x) dyn8[i] = tabs.dyn8[i];
@@ -541,9 +547,11 @@ __global__ void lm_stored_rows(const Nf4View W, const DecodeTables tabs, const i
   pdl_allow_next();
   pdl_wait();
   const float offset = W.dq ? *W.offset : 0.0f;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < M * D8;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < (M + kSamples) * D8;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t e = ids[i / D8] * D8 * 8 + i % D8 * 8;   // 8 elements of one 64-element block
+    const int64_t t = i / D8;
+    const int64_t row = t < M ? max(clean_target(targets[t], V, ignore), int64_t(0)) : sample_of(static_cast<int>(t - M), V);
+    const int64_t e = row * D8 * 8 + i % D8 * 8;   // 8 elements of one 64-element block
     const float s = block_scale(W, e / kBlock, dyn8, offset);
     const uint32_t q = *reinterpret_cast<const uint32_t*>(W.packed + e / 2);
     uint32_t o[4];
@@ -556,121 +564,178 @@ __global__ void lm_stored_rows(const Nf4View W, const DecodeTables tabs, const i
   }
 }
 
-// One warp per token: zt[t] = x[t] . W[y] in fp32; R's start (ref[0]); the pieces' spikes.
-// rows: W (row y), or with by_token the targets' decoded rows (row t).
-__global__ void lm_target(const uint4* x, const uint4* rows, int by_token, const int64_t* clean, int64_t M, int64_t D8,
-                          int f16, float* zt, float* ref, float* spike, int pieces) {
+__device__ __forceinline__ float dot8(uint4 u, uint4 v, int f16, float s) {
+  const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    s = fmaf(lo16(uu[k], f16), lo16(vv[k], f16), s);
+    s = fmaf(hi16(uu[k], f16), hi16(vv[k], f16), s);
+  }
+  return s;
+}
+
+constexpr int kPrepThreads = 128;
+
+// One CTA per token: clean[t]; zt[t] = x[t] . W[y] in fp32; R's start (ref, times log2(e), where a
+// gradient is asked for: kSample takes the samples' logits too); the pieces' spikes and flags.
+// A target outside [0, V) that is not ignore_index sets NF4_ERR_ARG.
+// rows: W, or with by_token the decoded rows of the targets and then of the samples.
+template <bool kSample>
+__global__ void __launch_bounds__(kPrepThreads)
+lm_prep(const uint4* x, const uint4* rows, int by_token, const int64_t* targets, int64_t M, int64_t V, int64_t ignore,
+        int64_t D8, int f16, int64_t* clean, float* zt, float* ref, float* spike, int* flags, int pieces, int tiles_t,
+        int* status) {
+  constexpr int kDots = kSample ? 1 + kSamples : 1;
+  __shared__ float red[kPrepThreads / 32][kDots];
   pdl_allow_next();
   pdl_wait();
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (t >= M) return;
-  const int64_t y = clean[t];
-  float s = 0.0f;
+  const int64_t t = blockIdx.x;
+  const int64_t given = targets[t], y = clean_target(given, V, ignore);
+  float s[kDots];
+#pragma unroll
+  for (int k = 0; k < kDots; ++k) s[k] = 0.0f;
   if (y >= 0) {
     const uint4* a = x + t * D8;
     const uint4* w = rows + (by_token ? t : y) * D8;
-    float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t i = lane; i < D8; i += 32) {
-      const uint4 u = a[i], v = w[i];
-      const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < D8; i += kPrepThreads) {
+      const uint4 u = a[i];
+      s[0] = dot8(u, w[i], f16, s[0]);
+      if (kSample) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        q[k] = fmaf(lo16(uu[k], f16), lo16(vv[k], f16), q[k]);
-        q[k] = fmaf(hi16(uu[k], f16), hi16(vv[k], f16), q[k]);
+        for (int k = 0; k < kDots - 1; ++k)
+          s[1 + k] = dot8(u, rows[(by_token ? M + k : sample_of(k, V)) * D8 + i], f16, s[1 + k]);
       }
     }
-    s = (q[0] + q[1]) + (q[2] + q[3]);
   }
-  s = warp_sum(s);
-  if (lane == 0) {
-    zt[t] = s;
-    if (ref != nullptr) ref[t] = s;
-  }
-  for (int c = lane; c < pieces; c += 32) spike[static_cast<int64_t>(c) * M + t] = -INFINITY;
-}
-
-// ref[t] = the larger of it and the first vocabulary tile's largest logit.
-__global__ void lm_raise_ref(float* ref, const float* part_max, int64_t M) {
-  pdl_allow_next();
-  pdl_wait();
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (t < M) ref[t] = fmaxf(ref[t], part_max[t]);
-}
-
-// One warp per token: its totals, loss, lse and dx's factors
-// coef[t] = {g / (others + own), g others / (others + own)}.
-// part_max given: each tile's sum is relative to that maximum; else to the R of its piece
-// (refs[piece + 1]), piece_tiles tiles a piece, and the result to the last R.
-__global__ void lm_rows(const float* part_sum, const float* part_max, const float* refs, int64_t M, int tiles,
-                        int piece_tiles, int pieces, const float* zt, const int64_t* clean, const float* gscale,
-                        int gscale_per_row, float* loss, float* lse, float2* coef) {
-  pdl_allow_next();
-  pdl_wait();
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (t >= M) return;
-  const bool live = clean[t] >= 0;
-  const float z = zt[t];
-  float ref;
-  float s = 0.0f;
-  if (part_max != nullptr) {
-    ref = z;
-    for (int i = lane; i < tiles; i += 32) ref = fmaxf(ref, part_max[static_cast<int64_t>(i) * M + t]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
-    for (int i = lane; i < tiles; i += 32) {
-      const float q = part_sum[static_cast<int64_t>(i) * M + t];
-      if (q != 0.0f) s += q * expf(part_max[static_cast<int64_t>(i) * M + t] - ref);
-    }
-  } else {
-    ref = refs[static_cast<int64_t>(pieces) * M + t];
-    for (int i = lane; i < tiles; i += 32) {
-      const float r = refs[static_cast<int64_t>(i / piece_tiles + 1) * M + t];
-      const float q = part_sum[static_cast<int64_t>(i) * M + t];
-      s += r == ref ? q : q * expf(r - ref);
-    }
+  for (int k = 0; k < kDots; ++k) {
+    s[k] = warp_sum(s[k]);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5][k] = s[k];
   }
-  const float others = warp_sum(s);
-  if (lane != 0) return;
-  const float own = expf(z - ref);
-  const float total = others + own;
-  // the quotient keeps the digits of a sure token's loss; far below the largest logit own vanishes
-  const float l = z - ref > -20.0f ? log1pf(others / own) : logf(total) + (ref - z);
-  loss[t] = live ? l : 0.0f;
-  if (lse != nullptr) lse[t] = live ? z + l : 0.0f;
-  if (coef != nullptr) {
-    const float g = gscale == nullptr ? 1.0f : gscale[gscale_per_row ? t : 0];
-    coef[t] = live ? make_float2(g / total, g * (others / total)) : make_float2(0.0f, 0.0f);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float z = 0.0f, top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kDots; ++k) {
+      float v = 0.0f;
+      for (int q = 0; q < kPrepThreads / 32; ++q) v += red[q][k];
+      if (k == 0) z = v;
+      top = fmaxf(top, v);
+    }
+    clean[t] = y;
+    zt[t] = z;
+    if (ref != nullptr) ref[t] = (kSample ? top : z) * kLog2e;
+    if (y < 0 && given != ignore) atomicCAS(status, 0, static_cast<int>(NF4_ERR_ARG));
+  }
+  for (int c = threadIdx.x; c < pieces; c += kPrepThreads) {
+    spike[static_cast<int64_t>(c) * M + t] = -INFINITY;
+    if (t < tiles_t) flags[c * tiles_t + t] = 0;
   }
 }
 
-// dx[t][d..d+7] = a (sum of the slices) - b W[y][d..d+7]; zero for a token that does not count.
-__global__ void lm_dx(const float4* acc, int slices, const uint4* rows, int by_token, const int64_t* clean,
-                      const float2* coef, int64_t M, int64_t D8, int f16, uint4* dx) {
+struct FinishArgs {
+  int64_t M, D8;
+  const float* part_sum;    // [parts][M]
+  const float* part_max;    // given: each part's sum is relative to it; else to its piece's R
+  const float* refs;        // [pieces + 1][M]: a piece's R is refs[piece + 1], the last is what dx's sums are relative to
+  int parts, piece_parts, pieces;
+  const float* zt;
+  const int64_t* clean;
+  const float* gscale;
+  int gscale_per_row;
+  float* loss;
+  float* lse;
+  const float4* acc;        // nullptr: no gradient
+  int slices;
+  const uint4* rows;
+  int by_token, f16;
+  uint4* dx;
+};
+constexpr int kFinThreads = 256, kFinTokens = 4;
+
+// kFinTokens tokens a CTA: each one's totals (64 threads down the parts, 16 bytes of neighbouring
+// tokens at a time), loss and lse, then dx of the CTA's share of the features (blockIdx.y):
+// dx[t][d] = a (sum of the slices) - b W[y][d], a = g / (others + own), b = others a.
+__global__ void __launch_bounds__(kFinThreads) lm_finish(const FinishArgs f) {
+  __shared__ float red[kFinThreads / 32][kFinTokens];
+  __shared__ float2 coef[kFinTokens];
+  __shared__ int64_t target[kFinTokens];
   pdl_allow_next();
   pdl_wait();
-  const int64_t n = M * D8;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t t = i / D8, d = i - t * D8;
-    const int64_t y = clean[t];
+  const int k = threadIdx.x % kFinTokens, i0 = threadIdx.x / kFinTokens, warp = threadIdx.x >> 5;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kFinTokens, t = t0 + k;
+  const bool in = t < f.M;
+  const float z = in ? f.zt[t] : 0.0f;
+  float ref = in && f.part_max == nullptr ? f.refs[static_cast<int64_t>(f.pieces) * f.M + t] : z * kLog2e;
+  if (f.part_max != nullptr) {
+    if (in)
+      for (int i = i0; i < f.parts; i += kFinThreads / kFinTokens)
+        ref = fmaxf(ref, f.part_max[static_cast<int64_t>(i) * f.M + t]);
+#pragma unroll
+    for (int o = 16; o >= kFinTokens; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+    if ((threadIdx.x & 31) < kFinTokens) red[warp][k] = ref;
+    __syncthreads();
+    for (int q = 0; q < kFinThreads / 32; ++q) ref = fmaxf(ref, red[q][k]);
+    __syncthreads();
+  }
+  float s = 0.0f;
+  if (in) {
+#pragma unroll 4
+    for (int i = i0; i < f.parts; i += kFinThreads / kFinTokens) {
+      const float q = f.part_sum[static_cast<int64_t>(i) * f.M + t];
+      const float r = f.part_max != nullptr ? f.part_max[static_cast<int64_t>(i) * f.M + t]
+                                            : f.refs[static_cast<int64_t>(i / f.piece_parts + 1) * f.M + t];
+      s += r == ref ? q : q == 0.0f ? 0.0f : q * exp2f(r - ref);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o >= kFinTokens; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) < kFinTokens) red[warp][k] = s;
+  __syncthreads();
+  if (threadIdx.x < kFinTokens) {
+    const bool live = in && f.clean[t] >= 0;
+    float others = 0.0f;
+    for (int q = 0; q < kFinThreads / 32; ++q) others += red[q][k];
+    const float d = fmaf(z, kLog2e, -ref);      // log2 of own
+    const float own = exp2f(d);
+    const float total = others + own;
+    // the quotient keeps the digits of a sure token's loss; far below the largest logit own vanishes
+    const float l = d > -28.0f ? log1pf(others / own) : fmaf(-kLn2, d, logf(total));
+    const float g = !live ? 0.0f : f.gscale == nullptr ? 1.0f : f.gscale[f.gscale_per_row ? t : 0];
+    coef[k] = make_float2(g / total, g * (others / total));
+    target[k] = live ? f.clean[t] : -1;
+    if (in && blockIdx.y == 0) {
+      f.loss[t] = live ? l : 0.0f;
+      if (f.lse != nullptr) f.lse[t] = live ? z + l : 0.0f;
+    }
+  }
+  if (f.acc == nullptr) return;
+  __syncthreads();
+  const int64_t n = f.M * f.D8;
+  const int64_t d0 = f.D8 * blockIdx.y / gridDim.y;
+  const int dn = static_cast<int>(f.D8 * (blockIdx.y + 1) / gridDim.y - d0);
+  for (int j = threadIdx.x; j < kFinTokens * dn; j += kFinThreads) {
+    const int tk = j / dn;
+    const int64_t d = d0 + j - tk * dn, at = (t0 + tk) * f.D8 + d, y = target[tk];
+    if (t0 + tk >= f.M) break;
     uint4 o = make_uint4(0, 0, 0, 0);
     if (y >= 0) {
-      const uint4 w = rows[(by_token ? t : y) * D8 + d];
-      float4 u = acc[2 * i], v = acc[2 * i + 1];
-      for (int q = 1; q < slices; ++q) {
-        const float4 a = acc[2 * (q * n + i)], b = acc[2 * (q * n + i) + 1];
+      const uint4 w = f.rows[(f.by_token ? t0 + tk : y) * f.D8 + d];
+      float4 u = f.acc[2 * at], v = f.acc[2 * at + 1];
+#pragma unroll 4
+      for (int q = 1; q < f.slices; ++q) {
+        const float4 a = f.acc[2 * (q * n + at)], b = f.acc[2 * (q * n + at) + 1];
         u.x += a.x, u.y += a.y, u.z += a.z, u.w += a.w;
         v.x += b.x, v.y += b.y, v.z += b.z, v.w += b.w;
       }
-      const float2 c = coef[t];
-      o.x = pack2(c.x * u.x - c.y * lo16(w.x, f16), c.x * u.y - c.y * hi16(w.x, f16), f16);
-      o.y = pack2(c.x * u.z - c.y * lo16(w.y, f16), c.x * u.w - c.y * hi16(w.y, f16), f16);
-      o.z = pack2(c.x * v.x - c.y * lo16(w.z, f16), c.x * v.y - c.y * hi16(w.z, f16), f16);
-      o.w = pack2(c.x * v.z - c.y * lo16(w.w, f16), c.x * v.w - c.y * hi16(w.w, f16), f16);
+      const float2 c = coef[tk];
+      o.x = pack2(c.x * u.x - c.y * lo16(w.x, f.f16), c.x * u.y - c.y * hi16(w.x, f.f16), f.f16);
+      o.y = pack2(c.x * u.z - c.y * lo16(w.y, f.f16), c.x * u.w - c.y * hi16(w.y, f.f16), f.f16);
+      o.z = pack2(c.x * v.x - c.y * lo16(w.z, f.f16), c.x * v.y - c.y * hi16(w.z, f.f16), f.f16);
+      o.w = pack2(c.x * v.z - c.y * lo16(w.w, f.f16), c.x * v.w - c.y * hi16(w.w, f.f16), f.f16);
     }
-    dx[i] = o;
+    f.dx[at] = o;
   }
 }
 
@@ -710,7 +775,7 @@ int grad_slices(int64_t tiles, int64_t cols) {
 struct LmLayout {
   int64_t Mb, cols;
   int pieces, tiles, slices, piece_tiles;
-  size_t clean, ids, zt, refs, spike, flags, part_sum, part_max, coef, wy, wb, P, acc, total;
+  size_t clean, zt, refs, spike, flags, part_sum, part_max, wy, wb, P, acc, total;
   LmLayout(int64_t M, int64_t V, int64_t D, bool stored, bool grad) {
     Mb = std::min(M, kBlockTokens);
     // without a gradient a piece only bounds the decoded copy of a stored head
@@ -728,15 +793,13 @@ struct LmLayout {
     };
     const size_t m = static_cast<size_t>(Mb);
     clean = take(8 * m);
-    ids = take(8 * m);
     zt = take(4 * m);
-    refs = take(4 * m * (pieces + 1));
-    spike = take(4 * m * pieces);
-    flags = take(sizeof(int) * static_cast<size_t>(tt) * pieces);
-    part_sum = take(4 * m * tiles);
-    part_max = take(4 * m * (grad ? 1 : tiles));
-    coef = take(grad ? 8 * m : 0);
-    wy = take(stored ? 2 * m * D : 0);
+    refs = take(grad ? 4 * m * (pieces + 1) : 0);
+    spike = take(grad ? 4 * m * pieces : 0);
+    flags = take(grad ? sizeof(int) * static_cast<size_t>(tt) * pieces : 0);
+    part_sum = take(4 * m * 2 * tiles);
+    part_max = take(grad ? 0 : 4 * m * 2 * tiles);
+    wy = take(stored ? 2 * (m + kSamples) * D : 0);
     wb = take(stored ? 2 * static_cast<size_t>(std::min(cols, V)) * D : 0);
     P = take(grad ? 2 * m * cols : 0);
     acc = take(grad ? sizeof(float) * m * D * slices : 0);
@@ -775,14 +838,12 @@ cudaError_t lm_loss(const LmLossArgs& a, void* ws, int* status, cudaStream_t st)
   const LmLayout L(a.M, a.V, a.D, stored, grad);
   char* w = static_cast<char*>(ws);
   auto* clean = reinterpret_cast<int64_t*>(w + L.clean);
-  auto* ids = reinterpret_cast<int64_t*>(w + L.ids);
   auto* zt = reinterpret_cast<float*>(w + L.zt);
   auto* refs = reinterpret_cast<float*>(w + L.refs);
   auto* spike = reinterpret_cast<float*>(w + L.spike);
   auto* flags = reinterpret_cast<int*>(w + L.flags);
   auto* part_sum = reinterpret_cast<float*>(w + L.part_sum);
   auto* part_max = reinterpret_cast<float*>(w + L.part_max);
-  auto* coef = grad ? reinterpret_cast<float2*>(w + L.coef) : nullptr;
   auto* acc = reinterpret_cast<float*>(w + L.acc);
   const CUtensorMapDataType dt = a.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
@@ -792,27 +853,22 @@ cudaError_t lm_loss(const LmLossArgs& a, void* ws, int* status, cudaStream_t st)
     const int64_t M = std::min(L.Mb, a.M - m0);
     const char* x = static_cast<const char*>(a.x) + 2 * m0 * a.D;
     const int tt = static_cast<int>((M + kTile - 1) / kTile);
-    note_launch();
-    if ((e = launch_pdl(lm_clean, dim3(static_cast<unsigned>((M + 255) / 256)), dim3(256), 0, st, 1, a.targets + m0, M,
-                        a.V, a.ignore_index, clean, ids, status)) != cudaSuccess)
-      return e;
     const void* rows = a.w16;
-    if (stored) {   // the targets' rows of a stored head
+    const int f16 = a.f16 ? 1 : 0;
+    if (stored) {
       rows = w + L.wy;
-      const int64_t ctas = std::min<int64_t>((M * D8 + 255) / 256, static_cast<int64_t>(device_sm_count()) * 8);
+      const int64_t ctas = std::min<int64_t>(((M + kSamples) * D8 + 255) / 256, static_cast<int64_t>(device_sm_count()) * 8);
       note_launch();
       if ((e = launch_pdl(lm_stored_rows, dim3(static_cast<unsigned>(ctas)), dim3(256), 0, st, 1, a.W, decode_tables(),
-                          static_cast<const int64_t*>(ids), M, D8, a.f16 ? 1 : 0,
-                          reinterpret_cast<uint4*>(w + L.wy))) != cudaSuccess)
+                          a.targets + m0, M, a.V, a.ignore_index, D8, f16, reinterpret_cast<uint4*>(w + L.wy))) !=
+          cudaSuccess)
         return e;
     }
     note_launch();
-    if ((e = launch_pdl(lm_target, dim3(static_cast<unsigned>((M + 7) / 8)), dim3(256), 0, st, 1,
-                        reinterpret_cast<const uint4*>(x), static_cast<const uint4*>(rows), stored ? 1 : 0,
-                        static_cast<const int64_t*>(clean), M, D8, a.f16 ? 1 : 0, zt, grad ? refs : nullptr, spike,
-                        grad ? L.pieces : 0)) != cudaSuccess)
-      return e;
-    if (grad && (e = cudaMemsetAsync(flags, 0, sizeof(int) * static_cast<size_t>(tt) * L.pieces, st)) != cudaSuccess)
+    if ((e = launch_pdl(grad && a.f16 ? lm_prep<true> : lm_prep<false>, dim3(static_cast<unsigned>(M)), dim3(kPrepThreads),
+                        0, st, 1, reinterpret_cast<const uint4*>(x), static_cast<const uint4*>(rows), stored ? 1 : 0,
+                        a.targets + m0, M, a.V, a.ignore_index, D8, f16, clean, zt, grad ? refs : nullptr, spike, flags,
+                        grad ? L.pieces : 0, tt, status)) != cudaSuccess)
       return e;
     CUtensorMap xm;
     if (!make_map(&xm, dt, x, a.D, M, 2 * a.D, kSub, kHalf, sw)) return cudaErrorInvalidValue;
@@ -833,7 +889,8 @@ cudaError_t lm_loss(const LmLossArgs& a, void* ws, int* status, cudaStream_t st)
       bool ok = make_map(&wm, dt, wc, a.D, cols, 2 * a.D, kSub, kHalf, sw);
       if (grad) {
         ok = ok && make_map(&wg, dt, wc, a.D, cols, 2 * a.D, kSub, kSub, sw);
-        ok = ok && make_map(&pm, dt, w + L.P, L.cols, M, 2 * L.cols, kSub, 32, sw);
+        ok = ok && make_map(&pm, dt, w + L.P, L.cols, M, 2 * L.cols, kBoxCols, 32,
+                            CU_TENSOR_MAP_SWIZZLE_64B);
         ok = ok && make_map(&pg, dt, w + L.P, L.cols, M, 2 * L.cols, kSub, kHalf, sw);
       } else {
         wg = pm = pg = wm;
@@ -853,21 +910,11 @@ cudaError_t lm_loss(const LmLossArgs& a, void* ws, int* status, cudaStream_t st)
       p.range = a.f16 ? kRangeF16 : kRangeBf16;
       p.targets = clean;
       p.status = status;
-      p.part_sum = part_sum + static_cast<int64_t>(c) * L.piece_tiles * M;
+      p.part_sum = part_sum + static_cast<int64_t>(c) * 2 * L.piece_tiles * M;
       if (!grad) {
-        p.part_max = part_max + static_cast<int64_t>(c) * L.piece_tiles * M;
+        p.part_max = part_max + static_cast<int64_t>(c) * 2 * L.piece_tiles * M;
         if ((e = launch_lm_gemm<kMax>(p, xm, wm, pm, st)) != cudaSuccess) return e;
         continue;
-      }
-      if (c == 0 && a.f16) {   // R's start from the first vocabulary tile too
-        LmParams q = p;
-        q.tiles_f = 1;
-        q.part_max = part_max;
-        if ((e = launch_lm_gemm<kMax>(q, xm, wm, pm, st)) != cudaSuccess) return e;
-        note_launch();
-        if ((e = launch_pdl(lm_raise_ref, dim3(static_cast<unsigned>((M + 255) / 256)), dim3(256), 0, st, 1, refs,
-                            static_cast<const float*>(part_max), M)) != cudaSuccess)
-          return e;
       }
       p.ref = refs + static_cast<int64_t>(c) * M;
       p.ref_next = refs + static_cast<int64_t>(c + 1) * M;
@@ -886,25 +933,34 @@ cudaError_t lm_loss(const LmLossArgs& a, void* ws, int* status, cudaStream_t st)
       g.acc = acc;
       if ((e = launch_lm_gemm<kGrad>(g, wg, pg, pm, st)) != cudaSuccess) return e;
     }
+    FinishArgs f{};
+    f.M = M;
+    f.D8 = D8;
+    f.part_sum = part_sum;
+    f.part_max = grad ? nullptr : part_max;
+    f.refs = refs;
+    f.parts = 2 * L.tiles;
+    f.piece_parts = 2 * L.piece_tiles;
+    f.pieces = L.pieces;
+    f.zt = zt;
+    f.clean = clean;
+    f.gscale = a.grad_scale == nullptr ? nullptr : a.grad_scale + (a.grad_scale_per_row ? m0 : 0);
+    f.gscale_per_row = a.grad_scale_per_row;
+    f.loss = a.loss + m0;
+    f.lse = a.lse == nullptr ? nullptr : a.lse + m0;
+    f.acc = grad ? reinterpret_cast<const float4*>(acc) : nullptr;
+    f.slices = L.slices;
+    f.rows = static_cast<const uint4*>(rows);
+    f.by_token = stored ? 1 : 0;
+    f.f16 = f16;
+    f.dx = reinterpret_cast<uint4*>(static_cast<char*>(a.dx) + 2 * m0 * a.D);
+    // few tokens: their features are shared among CTAs, each taking the totals again
+    const int64_t gx = (M + kFinTokens - 1) / kFinTokens;
+    const int64_t gy = grad ? std::max<int64_t>(1, std::min<int64_t>(4 * device_sm_count() / gx, D8 / 16)) : 1;
     note_launch();
-    if ((e = launch_pdl(lm_rows, dim3(static_cast<unsigned>((M + 7) / 8)), dim3(256), 0, st, 1,
-                        static_cast<const float*>(part_sum), grad ? nullptr : static_cast<const float*>(part_max),
-                        static_cast<const float*>(refs), M, L.tiles, L.piece_tiles, L.pieces,
-                        static_cast<const float*>(zt), static_cast<const int64_t*>(clean),
-                        a.grad_scale == nullptr ? nullptr : a.grad_scale + (a.grad_scale_per_row ? m0 : 0),
-                        a.grad_scale_per_row, a.loss + m0, a.lse == nullptr ? nullptr : a.lse + m0, coef)) != cudaSuccess)
+    if ((e = launch_pdl(lm_finish, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), dim3(kFinThreads), 0, st, 1,
+                        f)) != cudaSuccess)
       return e;
-    if (grad) {
-      const int64_t n = M * D8;
-      const int64_t ctas = std::min<int64_t>((n + 255) / 256, static_cast<int64_t>(device_sm_count()) * 8);
-      note_launch();
-      if ((e = launch_pdl(lm_dx, dim3(static_cast<unsigned>(ctas)), dim3(256), 0, st, 1,
-                          reinterpret_cast<const float4*>(acc), L.slices, static_cast<const uint4*>(rows),
-                          stored ? 1 : 0, static_cast<const int64_t*>(clean), static_cast<const float2*>(coef), M, D8,
-                          a.f16 ? 1 : 0, reinterpret_cast<uint4*>(static_cast<char*>(a.dx) + 2 * m0 * a.D))) !=
-          cudaSuccess)
-        return e;
-    }
   }
   return cudaGetLastError();
 }
