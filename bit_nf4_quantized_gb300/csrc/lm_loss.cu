@@ -413,35 +413,34 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
         const int valid = static_cast<int>(min(static_cast<int64_t>(kTile), p.cols - c_tile));
         const bool masked = __any_sync(0xffffffffu, yc >= 0) || valid < ce;
         const int64_t part = (static_cast<int64_t>(un.f) * 2 + half) * p.M + t;
-        auto mask = [&](uint32_t (&v)[32], int c0) {
-          if (masked) {
+        // the warp's whole part to registers, which frees the accumulator for the unit after next
+        uint32_t v[kEpiCols / 32][32];
+#pragma unroll
+        for (int h = 0; h < kEpiCols / 32; ++h) tmem_ld32(taddr + cb + 32 * h, v[h]);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(lead_bar(kBarAccEmpty + b));
+        if (masked) {
+#pragma unroll
+          for (int h = 0; h < kEpiCols / 32; ++h)
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (c0 + j == yc || c0 + j >= valid) v[j] = 0xff800000u;   // -inf
-          }
-        };
+              if (cb + 32 * h + j == yc || cb + 32 * h + j >= valid) v[h][j] = 0xff800000u;   // -inf
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int h = 0; h < kEpiCols / 32; ++h)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(v[h][j]));
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (MODE == kMax) {
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int c0 = cb; c0 < ce; c0 += 32) {
-            uint32_t v[32];
-            tmem_ld32(taddr + c0, v);
-            tmem_ld_wait();
-            mask(v, c0);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(v[j]));
-          }
           const float m2 = mx == -INFINITY ? 0.0f : mx * kLog2e;
-          float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-          for (int c0 = cb; c0 < ce; c0 += 32) {
-            uint32_t v[32];
-            tmem_ld32(taddr + c0, v);
-            tmem_ld_wait();
-            mask(v, c0);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(__uint_as_float(v[j]), kLog2e, -m2));
-          }
+          for (int h = 0; h < kEpiCols / 32; ++h)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(__uint_as_float(v[h][j]), kLog2e, -m2));
           if (t < p.M) {
             p.part_max[part] = mx == -INFINITY ? mx : m2;
             p.part_sum[part] = (s[0] + s[1]) + (s[2] + s[3]);
@@ -450,38 +449,32 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
           float r2 = t < p.M ? p.ref[t] : 0.0f;
           if (p.redo && t < p.M) r2 = fmaxf(r2, p.spike[t]);
           const uint32_t keep = live ? 0xffffffffu : 0u;
-          float mx = -INFINITY;
-          float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-          for (int c0 = cb; c0 < ce; c0 += kBoxCols, ++nst) {
+#pragma unroll
+          for (int h = 0; h < kEpiCols / kBoxCols; ++h, ++nst) {
             const uint32_t box = my_box + (nst & 1u) * kBoxBytes;
-            uint32_t v[32];
-            tmem_ld32(taddr + c0, v);
+            uint32_t o[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float e0 = ex2(fmaf(__uint_as_float(v[h][2 * k]), kLog2e, -r2));
+              const float e1 = ex2(fmaf(__uint_as_float(v[h][2 * k + 1]), kLog2e, -r2));
+              s[k & 3] += e0;
+              s[k & 3] += e1;
+              o[k] = pack2(e0, e1, p.f16) & keep;
+            }
             if (lane == 0) bulk_wait_read<1>();      // the store that last used this box has read it
             __syncwarp();
-            tmem_ld_wait();
-            mask(v, c0);
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              uint32_t o[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float z0 = __uint_as_float(v[j + 2 * k]), z1 = __uint_as_float(v[j + 2 * k + 1]);
-                mx = fmaxf(mx, fmaxf(z0, z1));
-                const float e0 = ex2(fmaf(z0, kLog2e, -r2)), e1 = ex2(fmaf(z1, kLog2e, -r2));
-                s[k] += e0;
-                s[k] += e1;
-                o[k] = pack2(e0, e1, p.f16) & keep;
-              }
-              // row `lane` of the box, 16-byte column j / 8, 64-byte swizzle
-              const uint32_t col = static_cast<uint32_t>(j / 8) ^ ((static_cast<uint32_t>(lane) >> 1) & 3u);
+            for (int k = 0; k < 4; ++k) {
+              // row `lane` of the box, 16-byte column k, 64-byte swizzle
+              const uint32_t col = static_cast<uint32_t>(k) ^ ((static_cast<uint32_t>(lane) >> 1) & 3u);
               asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * (kBoxCols * 2) + col * 16),
-                           "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                           "r"(o[4 * k]), "r"(o[4 * k + 1]), "r"(o[4 * k + 2]), "r"(o[4 * k + 3])
                            : "memory");
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
+              const int c0 = cb + h * kBoxCols;
               // the contraction over P goes on in zeros up to the next 64 columns
               if (t0w < p.M && c0 < (valid + kSub - 1) / kSub * kSub)
                 tma_store_2d(&tm_p, box, static_cast<int>(c_tile) + c0, static_cast<int>(t0w));
@@ -498,9 +491,11 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(lead_bar(kBarAccEmpty + b));
+      if (MODE == kGrad) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(lead_bar(kBarAccEmpty + b));
+      }
       ++lt;
     }
     if (MODE == kScores && lane == 0) bulk_wait_all();
@@ -679,6 +674,27 @@ __global__ void __launch_bounds__(kFinThreads) lm_finish(const FinishArgs f) {
     for (int q = 0; q < kFinThreads / 32; ++q) ref = fmaxf(ref, red[q][k]);
     __syncthreads();
   }
+  // dx's items of this CTA (8 features of one token each); a thread's first one is gathered while
+  // the totals' loads are under way
+  const int64_t n = f.M * f.D8;
+  const int64_t d0 = f.D8 * blockIdx.y / gridDim.y;
+  const int dn = f.acc == nullptr ? 0 : static_cast<int>(f.D8 * (blockIdx.y + 1) / gridDim.y - d0);
+  const int items = static_cast<int>(min(static_cast<int64_t>(kFinTokens), f.M - t0)) * dn;
+  float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = u;
+  uint4 w = make_uint4(0, 0, 0, 0);
+  auto gather = [&](int j) {
+    const int tk = j / dn;
+    const int64_t d = d0 + j - tk * dn, at = (t0 + tk) * f.D8 + d, y = f.clean[t0 + tk];
+    w = f.rows[(f.by_token ? t0 + tk : max(y, int64_t(0))) * f.D8 + d];
+    u = f.acc[2 * at], v = f.acc[2 * at + 1];
+#pragma unroll 4
+    for (int q = 1; q < f.slices; ++q) {
+      const float4 a = f.acc[2 * (q * n + at)], b = f.acc[2 * (q * n + at) + 1];
+      u.x += a.x, u.y += a.y, u.z += a.z, u.w += a.w;
+      v.x += b.x, v.y += b.y, v.z += b.z, v.w += b.w;
+    }
+  };
+  if (threadIdx.x < items) gather(threadIdx.x);
   float s = 0.0f;
   if (in) {
 #pragma unroll 4
@@ -710,32 +726,19 @@ __global__ void __launch_bounds__(kFinThreads) lm_finish(const FinishArgs f) {
       if (f.lse != nullptr) f.lse[t] = live ? z + l : 0.0f;
     }
   }
-  if (f.acc == nullptr) return;
   __syncthreads();
-  const int64_t n = f.M * f.D8;
-  const int64_t d0 = f.D8 * blockIdx.y / gridDim.y;
-  const int dn = static_cast<int>(f.D8 * (blockIdx.y + 1) / gridDim.y - d0);
-  for (int j = threadIdx.x; j < kFinTokens * dn; j += kFinThreads) {
+  for (int j = threadIdx.x; j < items; j += kFinThreads) {
+    if (j != threadIdx.x) gather(j);
     const int tk = j / dn;
-    const int64_t d = d0 + j - tk * dn, at = (t0 + tk) * f.D8 + d, y = target[tk];
-    if (t0 + tk >= f.M) break;
     uint4 o = make_uint4(0, 0, 0, 0);
-    if (y >= 0) {
-      const uint4 w = f.rows[(f.by_token ? t0 + tk : y) * f.D8 + d];
-      float4 u = f.acc[2 * at], v = f.acc[2 * at + 1];
-#pragma unroll 4
-      for (int q = 1; q < f.slices; ++q) {
-        const float4 a = f.acc[2 * (q * n + at)], b = f.acc[2 * (q * n + at) + 1];
-        u.x += a.x, u.y += a.y, u.z += a.z, u.w += a.w;
-        v.x += b.x, v.y += b.y, v.z += b.z, v.w += b.w;
-      }
+    if (target[tk] >= 0) {
       const float2 c = coef[tk];
       o.x = pack2(c.x * u.x - c.y * lo16(w.x, f.f16), c.x * u.y - c.y * hi16(w.x, f.f16), f.f16);
       o.y = pack2(c.x * u.z - c.y * lo16(w.y, f.f16), c.x * u.w - c.y * hi16(w.y, f.f16), f.f16);
       o.z = pack2(c.x * v.x - c.y * lo16(w.z, f.f16), c.x * v.y - c.y * hi16(w.z, f.f16), f.f16);
       o.w = pack2(c.x * v.z - c.y * lo16(w.w, f.f16), c.x * v.w - c.y * hi16(w.w, f.f16), f.f16);
     }
-    f.dx[at] = o;
+    f.dx[(t0 + tk) * f.D8 + d0 + j - tk * dn] = o;
   }
 }
 
