@@ -8,6 +8,7 @@ missing or a call fails, an exception is raised.
 """
 
 import ctypes
+import importlib.util
 import os
 from dataclasses import dataclass
 
@@ -563,96 +564,12 @@ def qlora_bwd_batch_workspace_bytes(M: int, shapes, rank: int, dtype=torch.bfloa
 
 # ---- around the linear: the norm, 8-bit activation checkpoints, the loss ----------------------
 
+# These calls are marshalled by the compiled _torch_ops module (csrc/host/torch_ops.cpp): it checks
+# the arguments (ValueError, or TypeError for a dtype no call takes), copies strided or misaligned
+# inputs, allocates what is not given, records every tensor on a stream other than the current
+# one, and calls the C ABI (Nf4Error on a status other than NF4_OK).
+
 ACT8_BLOCK = 128
-
-
-class _Call:
-    """The tensors of one call: checked, made contiguous where the call only reads them, and
-    kept from reuse while another stream than the current one may still work on them.
-
-    Small calls are bound by this code (a launch takes 3 us of the host, an allocation 1.5), so
-    the current stream is read as a raw handle (0.1 us, against 2 for a Stream object) and the
-    device is only switched where it is not the current one."""
-
-    __slots__ = ("name", "device", "index", "stream", "side")
-
-    def __init__(self, name, t, stream):
-        if not t.is_cuda:
-            raise ValueError(f"{name}: CUDA tensors expected, got one on {t.device}")
-        self.name, self.device, self.index = name, t.device, t.get_device()
-        current = torch._C._cuda_getCurrentRawStream(self.index)
-        self.stream = current if stream is None else stream.cuda_stream
-        self.side = None if self.stream == current else stream
-
-    def _refuse(self, what, t, shape, dtype):
-        if not isinstance(t, torch.Tensor) or t.device != self.device:
-            raise ValueError(f"{self.name}: {what} must be a tensor on {self.device}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{self.name}: {what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        raise ValueError(f"{self.name}: {what} is {t.dtype}, expected {dtype}")
-
-    def read(self, what, t, shape, dtype):
-        """An input; a strided or misaligned one is copied (on the call's stream)."""
-        if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype or t.device != self.device:
-            self._refuse(what, t, shape, dtype)
-        if self.side is not None:
-            t.record_stream(self.side)
-        if not t.is_contiguous() or t.data_ptr() & 15:
-            if self.side is None:
-                return t.clone(memory_format=torch.contiguous_format)
-            with torch.cuda.stream(self.side):
-                return t.clone(memory_format=torch.contiguous_format)
-        return t
-
-    def written(self, what, t, shape, dtype):
-        """An output: the caller's (contiguous) or a new one."""
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=self.device)
-        else:
-            if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype or t.device != self.device:
-                self._refuse(what, t, shape, dtype)
-            if not t.is_contiguous():
-                raise ValueError(f"{self.name}: {what} must be contiguous")
-        if self.side is not None:
-            t.record_stream(self.side)
-        return t
-
-    def stored(self, W):
-        """The C struct of an Nf4Tensor input."""
-        if self.side is not None:
-            for t in (W.packed, W.absmax, W.nested_absmax, W.offset):
-                if t is not None:
-                    t.record_stream(self.side)
-        return W.c_struct()
-
-    def act8(self, c, shape, write):
-        """The C struct of a checkpoint, and the tensors to keep until the call is made."""
-        if not isinstance(c, Act8):
-            raise ValueError(f"{self.name}: an Act8 expected")
-        take = self.written if write else self.read
-        M, K = shape
-        codes = take("codes", c.codes, shape, torch.int8)
-        scales = take("scales", c.scales, (M, (K + ACT8_BLOCK - 1) // ACT8_BLOCK), torch.float32)
-        return _Act8(M, K, codes.data_ptr(), scales.data_ptr()), (codes, scales)
-
-    def workspace(self, given, query, *sizes):
-        ws = torch.empty(max(query(*sizes), 16), dtype=torch.uint8, device=self.device) if given is None else given
-        if self.side is not None:
-            ws.record_stream(self.side)
-        return ws
-
-    def run(self, fn, *args):
-        if self.index == torch.cuda.current_device():
-            status = fn(*args, self.stream)
-        else:
-            with torch.cuda.device(self.device):
-                status = fn(*args, self.stream)
-        if status != NF4_OK:
-            raise Nf4Error(status, self.name)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 @dataclass
@@ -675,53 +592,41 @@ class Act8:
                     torch.empty((M, -(-K // ACT8_BLOCK)), dtype=torch.float32, device=device))
 
 
-def _matrix(name, t, what="x"):
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError(f"{name}: {what} must be a 2-D tensor")
-    return t.shape
+_OPS = None
+
+
+def _ops():
+    """The compiled marshalling module (built next to the library)."""
+    global _OPS
+    if _OPS is None:
+        load()
+        path = _build.HOST_LIB
+        if not os.path.exists(path):
+            raise RuntimeError(f"_torch_ops.so is not built ({path}); run bit_nf4_quantized_gb300.build")
+        spec = importlib.util.spec_from_file_location("_torch_ops", path)
+        ops = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ops)
+        ops.init(Nf4Error, Act8, Nf4Tensor)
+        _OPS = ops
+    return _OPS
 
 
 def qlora_act8_quantize(x: torch.Tensor, out: Act8 = None, stream=None) -> Act8:
     """x [M, K] (float32, bf16 or half) stored as int8 codes with one scale per 128 columns."""
-    lib = load()
-    M, K = _matrix("qlora_act8_quantize", x)
-    call = _Call("qlora_act8_quantize", x, stream)
-    x = call.read("x", x, (M, K), x.dtype)
-    out = Act8.empty(M, K, x.device) if out is None else out
-    cs, _keep = call.act8(out, (M, K), True)
-    call.run(lib.qlora_act8_quantize, _addr(x), _dtype_code(x.dtype), ctypes.byref(cs))
-    return out
+    return (_OPS or _ops()).act8_quantize(x, out, stream)
 
 
 def qlora_act8_dequantize(c: Act8, dtype=torch.bfloat16, weight: torch.Tensor = None, out: torch.Tensor = None,
                           stream=None) -> torch.Tensor:
     """The values a checkpoint stands for (times weight [K] where given), [M, K] in dtype."""
-    lib = load()
-    M, K = c.shape
-    call = _Call("qlora_act8_dequantize", c.codes, stream)
-    cs, _keep = call.act8(c, (M, K), False)
-    weight = None if weight is None else call.read("weight", weight, (K,), torch.float32)
-    y = call.written("out", out, (M, K), dtype if out is None else out.dtype)
-    call.run(lib.qlora_act8_dequantize, ctypes.byref(cs), _addr(weight), _addr(y), _dtype_code(y.dtype))
-    return y
+    return (_OPS or _ops()).act8_dequantize(c, dtype, weight, out, stream)
 
 
 def qlora_act8_grad_a(G: torch.Tensor, c: Act8, alpha: float, mode: int = SCALE_LORA, weight: torch.Tensor = None,
                       dA: torch.Tensor = None, workspace: torch.Tensor = None, stream=None) -> torch.Tensor:
     """dA = s G^T x [r, K] of an adapter whose input x is a checkpoint (times weight [K] where
     given); G = dY B is float32 [M, r]."""
-    lib = load()
-    M, K = c.shape
-    r = _matrix("qlora_act8_grad_a", G, "G")[1]
-    call = _Call("qlora_act8_grad_a", G, stream)
-    G = call.read("G", G, (M, r), torch.float32)
-    cs, _keep = call.act8(c, (M, K), False)
-    weight = None if weight is None else call.read("weight", weight, (K,), torch.float32)
-    dA = call.written("dA", dA, (r, K), torch.float32)
-    ws = call.workspace(workspace, lib.qlora_act8_grad_a_workspace_bytes, M, K, r)
-    call.run(lib.qlora_act8_grad_a, r, alpha, mode, _addr(G), ctypes.byref(cs), _addr(weight), _addr(dA),
-             _addr(ws), ws.numel())
-    return dA
+    return (_OPS or _ops()).act8_grad_a(G, c, alpha, mode, weight, dA, workspace, stream)
 
 
 def qlora_linear_bwd_act8(dy: torch.Tensor, c: Act8, T: torch.Tensor, W, A: torch.Tensor, B: torch.Tensor,
@@ -731,31 +636,7 @@ def qlora_linear_bwd_act8(dy: torch.Tensor, c: Act8, T: torch.Tensor, W, A: torc
     """qlora_linear_bwd with the input x kept as a checkpoint (times weight [K], the norm's,
     where the checkpoint holds the normalised rows).  W is an Nf4Tensor, or the decoded weight
     [N, K] in dy's dtype.  Returns (dX, dA, dB)."""
-    lib = load()
-    name = "qlora_linear_bwd_act8"
-    M, N = _matrix(name, dy, "dy")
-    r, K = _matrix(name, A, "A")
-    call = _Call(name, dy, stream)
-    dy = call.read("dy", dy, (M, N), dy.dtype)
-    cs, _keep = call.act8(c, (M, K), False)
-    weight = None if weight is None else call.read("weight", weight, (K,), torch.float32)
-    T = call.read("T", T, (M, r), torch.float32)
-    A = call.read("A", A, (r, K), torch.float32)
-    B = call.read("B", B, (N, r), torch.float32)
-    stored = isinstance(W, Nf4Tensor)
-    if stored and tuple(W.shape) != (N, K):
-        raise ValueError(f"{name}: W has shape {tuple(W.shape)}, expected {(N, K)}")
-    w16 = None if stored else call.read("W", W, (N, K), dy.dtype)
-    wcs = call.stored(W) if stored else None
-    dx = call.written("dx", dx, (M, K), dy.dtype)
-    dA = call.written("dA", dA, (r, K), torch.float32)
-    dB = call.written("dB", dB, (N, r), torch.float32)
-    cd = _dtype_code(dy.dtype)
-    ws = call.workspace(workspace, lib.qlora_bwd_act8_workspace_bytes, M, N, K, r, cd, int(not stored))
-    call.run(lib.qlora_linear_bwd_act8, M, N, K, r, alpha, mode, cd, _addr(dy), ctypes.byref(cs),
-             _addr(weight), _addr(T), ctypes.byref(wcs) if stored else None, _addr(w16), _addr(A), _addr(B), _addr(dx),
-             _addr(dA), _addr(dB), _addr(ws), ws.numel())
-    return dx, dA, dB
+    return (_OPS or _ops()).linear_bwd_act8(dy, c, T, W, A, B, alpha, mode, weight, dx, dA, dB, workspace, stream)
 
 
 def qlora_rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor = None,
@@ -765,29 +646,7 @@ def qlora_rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5,
 
     x, residual [M, K]; weight [K] float32.  Without a residual h is x itself.  ``checkpoint``:
     True or an Act8 stores the normalised rows h / rms(h), before the weight, in 8 bits."""
-    lib = load()
-    name = "qlora_rms_norm_fwd"
-    M, K = _matrix(name, x)
-    call = _Call(name, x, stream)
-    dt = x.dtype
-    given = x
-    x = call.read("x", x, (M, K), dt)
-    residual = None if residual is None else call.read("residual", residual, (M, K), dt)
-    weight = call.read("weight", weight, (K,), torch.float32)
-    y = call.written("y", y, (M, K), dt)
-    rstd = call.written("rstd", rstd, (M,), torch.float32)
-    stored = residual is not None or h is not None
-    h = call.written("h", h, (M, K), dt) if stored else given
-    cs = None
-    if checkpoint is True:
-        checkpoint = Act8.empty(M, K, x.device)
-    elif checkpoint is False:
-        checkpoint = None
-    if checkpoint is not None:
-        cs, _keep = call.act8(checkpoint, (M, K), True)
-    call.run(lib.qlora_rms_norm_fwd, M, K, eps, _dtype_code(dt), _addr(x), _addr(residual), _addr(weight),
-             _addr(y), _addr(h) if stored else None, _addr(rstd), None if cs is None else ctypes.byref(cs))
-    return y, h, rstd, checkpoint
+    return (_OPS or _ops()).rms_norm_fwd(x, weight, eps, residual, checkpoint, y, h, rstd, stream)
 
 
 def qlora_rms_norm_bwd(dy: torch.Tensor, saved, rstd: torch.Tensor, weight: torch.Tensor,
@@ -796,31 +655,7 @@ def qlora_rms_norm_bwd(dy: torch.Tensor, saved, rstd: torch.Tensor, weight: torc
     """Returns (dx, dweight) of qlora_rms_norm_fwd.  ``saved``: the forward's h or its checkpoint
     (an Act8); ``dresidual``: the gradient that reaches h by the residual path; ``dweight``:
     True or a float32 [K] tensor computes the weight's gradient."""
-    lib = load()
-    name = "qlora_rms_norm_bwd"
-    M, K = _matrix(name, dy, "dy")
-    call = _Call(name, dy, stream)
-    dt = dy.dtype
-    dy = call.read("dy", dy, (M, K), dt)
-    cs = h = None
-    if isinstance(saved, Act8):
-        cs, _keep = call.act8(saved, (M, K), False)
-    else:
-        h = call.read("h", saved, (M, K), dt)
-    rstd = call.read("rstd", rstd, (M,), torch.float32)
-    weight = call.read("weight", weight, (K,), torch.float32)
-    dresidual = None if dresidual is None else call.read("dresidual", dresidual, (M, K), dt)
-    dx = call.written("dx", dx, (M, K), dt)
-    ws = None
-    if dweight is None or dweight is False:
-        dweight = None
-    else:
-        dweight = call.written("dweight", None if dweight is True else dweight, (K,), torch.float32)
-        ws = call.workspace(workspace, lib.qlora_rms_norm_bwd_workspace_bytes, M, K)
-    call.run(lib.qlora_rms_norm_bwd, M, K, _dtype_code(dt), _addr(dy), _addr(h), None if cs is None else ctypes.byref(cs),
-             _addr(rstd), _addr(weight), _addr(dresidual), _addr(dx), _addr(dweight), _addr(ws),
-             0 if ws is None else ws.numel())
-    return dx, dweight
+    return (_OPS or _ops()).rms_norm_bwd(dy, saved, rstd, weight, dresidual, dweight, dx, workspace, stream)
 
 
 def qlora_lm_loss(x: torch.Tensor, W, targets: torch.Tensor, grad_scale: torch.Tensor = None, ignore_index: int = -100,
@@ -830,33 +665,10 @@ def qlora_lm_loss(x: torch.Tensor, W, targets: torch.Tensor, grad_scale: torch.T
 
     x [M, D] bf16 or half; W [V, D] in x's dtype, or an Nf4Tensor; targets [M] int64, where
     ``ignore_index`` marks a token that does not count (loss, lse and dx are zero).
-    ``grad_scale``: float32 [M] or [1], what dx is multiplied with (None: 1).  loss and lse are
-    float32 [M]; dx is None with need_dx=False.  A target outside the vocabulary sets the device
-    status word and counts as ignored."""
-    lib = load()
-    name = "qlora_lm_loss"
-    M, D = _matrix(name, x)
-    call = _Call(name, x, stream)
-    x = call.read("x", x, (M, D), x.dtype)
-    stored = isinstance(W, Nf4Tensor)
-    V = (W.shape if stored else _matrix(name, W, "W"))[0]
-    if stored and tuple(W.shape) != (V, D):
-        raise ValueError(f"{name}: W has shape {tuple(W.shape)}, expected {(V, D)}")
-    w16 = None if stored else call.read("W", W, (V, D), x.dtype)
-    wcs = call.stored(W) if stored else None
-    targets = call.read("targets", targets, (M,), torch.int64)
-    per_row = 0
-    if grad_scale is not None:
-        per_row = int(grad_scale.numel() != 1)
-        grad_scale = call.read("grad_scale", grad_scale.reshape(-1), (M if per_row else 1,), torch.float32)
-    loss = call.written("loss", loss, (M,), torch.float32)
-    lse = call.written("lse", lse, (M,), torch.float32)
-    dx = call.written("dx", dx, (M, D), x.dtype) if need_dx else None
-    ws = call.workspace(workspace, lib.qlora_lm_loss_workspace_bytes, M, V, D, int(stored), int(need_dx))
-    call.run(lib.qlora_lm_loss, M, V, D, _dtype_code(x.dtype), _addr(x), ctypes.byref(wcs) if stored else None,
-             _addr(w16), _addr(targets), ignore_index, _addr(grad_scale), per_row, _addr(loss), _addr(lse), _addr(dx),
-             _addr(ws), ws.numel())
-    return loss, lse, dx
+    ``grad_scale``: float32 [M], or one value on the device, what dx is multiplied with (None:
+    1).  loss and lse are float32 [M]; dx is None with need_dx=False.  A target outside the
+    vocabulary sets the device status word and counts as ignored."""
+    return (_OPS or _ops()).lm_loss(x, W, targets, grad_scale, ignore_index, need_dx, loss, lse, dx, workspace, stream)
 
 
 def debug_wait_timeout(on: bool = True):

@@ -1,0 +1,508 @@
+// Torch entry points of the operators around the linear: argument checks, outputs and workspaces,
+// the current stream, and the call of the C ABI.  Marshalling only, like binding.py's ctypes
+// layer, but compiled: a small call is bound by the host (a one-token norm's kernel takes 3 us),
+// and its checks and allocations took 13 us in Python against 5 here.
+//
+// Every function takes all of its arguments by position (binding.py holds the signatures and
+// their documentation).  Inputs are checked for device, shape and type; a strided or misaligned
+// one is copied on the call's stream.  Outputs given by the caller must be contiguous.  With a
+// stream other than the current one, every tensor is recorded on it, so that its memory is not
+// reused too early.
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+
+#include <optional>
+#include <string>
+
+#include "qlora_nf4.h"
+
+namespace {
+
+using at::Tensor;
+
+PyObject* g_nf4_error = nullptr;   // binding.Nf4Error(status, where)
+PyObject* g_act8 = nullptr;        // binding.Act8(codes, scales)
+PyObject* g_nf4_tensor = nullptr;  // binding.Nf4Tensor
+
+struct PyError {};                 // a Python exception is set
+
+[[noreturn]] void refuse(PyObject* type, const std::string& text) {
+  PyErr_SetString(type, text.c_str());
+  throw PyError{};
+}
+
+std::string shape_text(at::IntArrayRef s) {
+  std::string t = "(";
+  for (size_t i = 0; i < s.size(); ++i) t += (i ? ", " : "") + std::to_string(s[i]);
+  return t + (s.size() == 1 ? ",)" : ")");
+}
+
+nf4_dtype dtype_code(at::ScalarType t) {
+  switch (t) {
+    case at::kFloat: return NF4_F32;
+    case at::kBFloat16: return NF4_BF16;
+    case at::kHalf: return NF4_F16;
+    default: refuse(PyExc_TypeError, std::string("unsupported dtype ") + c10::toString(t));
+  }
+}
+
+const Tensor* tensor_of(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
+
+// A tensor whose sizes the call takes its own from.
+const Tensor& matrix(const char* name, const char* what, PyObject* o) {
+  const Tensor* t = tensor_of(o);
+  if (t == nullptr || t->dim() != 2) refuse(PyExc_ValueError, std::string(name) + ": " + what + " must be a 2-D tensor");
+  return *t;
+}
+
+struct OwnedRef {
+  PyObject* p = nullptr;
+  explicit OwnedRef(PyObject* o) : p(o) {
+    if (o == nullptr) throw PyError{};
+  }
+  OwnedRef(OwnedRef&& o) : p(o.p) { o.p = nullptr; }
+  OwnedRef(const OwnedRef&) = delete;
+  ~OwnedRef() { Py_XDECREF(p); }
+};
+
+class Call {
+ public:
+  Call(const char* name, const Tensor& first, PyObject* stream) : name_(name), device_(first.device()) {
+    if (!device_.is_cuda()) refuse(PyExc_ValueError, where() + "CUDA tensors expected, got one on " + device_.str());
+    guard_.set_device(device_);
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(device_.index());
+    stream_ = current.stream();
+    if (stream != Py_None) {
+      OwnedRef id(PyObject_GetAttrString(stream, "stream_id")), dev(PyObject_GetAttrString(stream, "device_index"));
+      const c10::cuda::CUDAStream given(
+          c10::Stream::unpack3(PyLong_AsLongLong(id.p), static_cast<c10::DeviceIndex>(PyLong_AsLong(dev.p)), c10::kCUDA));
+      if (PyErr_Occurred()) throw PyError{};
+      stream_ = given.stream();
+      if (given != current) side_ = given;
+    }
+  }
+
+  at::ScalarType type_of(PyObject* o, const char* what) {
+    const Tensor* t = tensor_of(o);
+    if (t == nullptr) refuse(PyExc_ValueError, where() + what + " must be a tensor");
+    return t->scalar_type();
+  }
+
+  // An input; a strided or misaligned one is copied (on the call's stream).
+  Tensor read(const char* what, PyObject* o, at::IntArrayRef shape, at::ScalarType type) {
+    const Tensor& t = check(what, o, shape, type);
+    use(t);
+    if (t.is_contiguous() && (reinterpret_cast<uintptr_t>(t.data_ptr()) & 15u) == 0) return t;
+    std::optional<c10::cuda::CUDAStreamGuard> on;
+    if (side_) on.emplace(*side_);
+    return t.clone(at::MemoryFormat::Contiguous);
+  }
+  Tensor read_or_none(const char* what, PyObject* o, at::IntArrayRef shape, at::ScalarType type) {
+    return o == Py_None ? Tensor() : read(what, o, shape, type);
+  }
+
+  // An output: the caller's (contiguous) or a new one.
+  Tensor written(const char* what, PyObject* o, at::IntArrayRef shape, at::ScalarType type) {
+    Tensor t;
+    if (o == Py_None) {
+      t = at::empty(shape, at::TensorOptions().dtype(type).device(device_));
+    } else {
+      t = check(what, o, shape, type);
+      if (!t.is_contiguous()) refuse(PyExc_ValueError, where() + what + " must be contiguous");
+    }
+    use(t);
+    return t;
+  }
+
+  // The caller's workspace or a new one.
+  Tensor workspace(PyObject* o, size_t need) {
+    Tensor t;
+    if (o == Py_None) {
+      const int64_t n = static_cast<int64_t>(need < 16 ? 16 : need);
+      t = at::empty({n}, at::TensorOptions().dtype(at::kByte).device(device_));
+    } else {
+      const Tensor* g = tensor_of(o);
+      if (g == nullptr || g->device() != device_ || g->scalar_type() != at::kByte || !g->is_contiguous())
+        refuse(PyExc_ValueError, where() + "workspace must be a contiguous uint8 tensor on " + device_.str());
+      t = *g;
+    }
+    use(t);
+    return t;
+  }
+
+  void use(const Tensor& t) {
+    if (side_ && t.defined()) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *side_);
+  }
+
+  void done(nf4_status s) {
+    if (s == NF4_OK) return;
+    OwnedRef e(PyObject_CallFunction(g_nf4_error, "is", static_cast<int>(s), name_));
+    PyErr_SetObject(g_nf4_error, e.p);
+    throw PyError{};
+  }
+
+  void* stream() const { return stream_; }
+  std::string where() const { return std::string(name_) + ": "; }
+
+ private:
+  const Tensor& check(const char* what, PyObject* o, at::IntArrayRef shape, at::ScalarType type) {
+    const Tensor* t = tensor_of(o);
+    if (t == nullptr || t->device() != device_)
+      refuse(PyExc_ValueError, where() + what + " must be a tensor on " + device_.str());
+    if (t->sizes() != shape)
+      refuse(PyExc_ValueError, where() + what + " has shape " + shape_text(t->sizes()) + ", expected " + shape_text(shape));
+    if (t->scalar_type() != type)
+      refuse(PyExc_ValueError, where() + what + " is " + c10::toString(t->scalar_type()) + ", expected " + c10::toString(type));
+    return *t;
+  }
+
+  const char* name_;
+  c10::Device device_;
+  c10::cuda::OptionalCUDAGuard guard_;
+  cudaStream_t stream_ = nullptr;
+  std::optional<c10::cuda::CUDAStream> side_;
+};
+
+float* f32(const Tensor& t) { return t.defined() ? static_cast<float*>(t.data_ptr()) : nullptr; }
+void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+int64_t scale_cols(int64_t K) { return (K + 127) / 128; }
+
+// A checkpoint argument or result.
+struct Act8 {
+  Tensor codes, scales;
+  qlora_act8 c() const {
+    return qlora_act8{codes.size(0), codes.size(1), static_cast<int8_t*>(codes.data_ptr()), f32(scales)};
+  }
+};
+
+bool is_act8(PyObject* o) { return PyObject_TypeCheck(o, reinterpret_cast<PyTypeObject*>(g_act8)); }
+
+Act8 act8_arg(Call& call, PyObject* o, int64_t M, int64_t K, bool write) {
+  if (!is_act8(o)) refuse(PyExc_ValueError, call.where() + "an Act8 expected");
+  OwnedRef codes(PyObject_GetAttrString(o, "codes")), scales(PyObject_GetAttrString(o, "scales"));
+  if (write)
+    return Act8{call.written("codes", codes.p, {M, K}, at::kChar),
+                call.written("scales", scales.p, {M, scale_cols(K)}, at::kFloat)};
+  return Act8{call.read("codes", codes.p, {M, K}, at::kChar), call.read("scales", scales.p, {M, scale_cols(K)}, at::kFloat)};
+}
+
+Act8 act8_new(Call& call, int64_t M, int64_t K) {
+  return Act8{call.written("codes", Py_None, {M, K}, at::kChar),
+              call.written("scales", Py_None, {M, scale_cols(K)}, at::kFloat)};
+}
+
+PyObject* wrap(const Tensor& t) {
+  if (!t.defined()) Py_RETURN_NONE;
+  return THPVariable_Wrap(t);
+}
+
+PyObject* wrap(const Act8& a) {
+  OwnedRef codes(wrap(a.codes)), scales(wrap(a.scales));
+  PyObject* argv[2] = {codes.p, scales.p};
+  return PyObject_Vectorcall(g_act8, argv, 2, nullptr);
+}
+
+PyObject* pack(std::initializer_list<PyObject*> items) {   // steals the references
+  PyObject* t = PyTuple_New(static_cast<Py_ssize_t>(items.size()));
+  Py_ssize_t i = 0;
+  for (PyObject* o : items) PyTuple_SET_ITEM(t, i++, o);
+  return t;
+}
+
+PyObject* same(PyObject* o) {
+  Py_INCREF(o);
+  return o;
+}
+
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw PyError{};
+  return v;
+}
+int64_t whole(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw PyError{};
+  return v;
+}
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw PyError{};
+  return v != 0;
+}
+
+// An Nf4Tensor argument: the C struct and the tensors it points into.
+struct Stored {
+  nf4_tensor t{};
+  Tensor keep[4];
+  int64_t rows = 0, cols = 0;
+};
+Stored stored_arg(Call& call, PyObject* o) {
+  Stored s;
+  OwnedRef shape(PyObject_GetAttrString(o, "shape")), dq(PyObject_GetAttrString(o, "double_quant"));
+  if (!PyTuple_Check(shape.p) || PyTuple_GET_SIZE(shape.p) != 2)
+    refuse(PyExc_ValueError, call.where() + "a 2-D Nf4Tensor expected");
+  s.rows = whole(PyTuple_GET_ITEM(shape.p, 0));
+  s.cols = whole(PyTuple_GET_ITEM(shape.p, 1));
+  const char* names[4] = {"packed", "absmax", "nested_absmax", "offset"};
+  for (int i = 0; i < 4; ++i) {
+    OwnedRef a(PyObject_GetAttrString(o, names[i]));
+    if (a.p == Py_None) continue;
+    const Tensor* t = tensor_of(a.p);
+    if (t == nullptr) refuse(PyExc_ValueError, call.where() + names[i] + " must be a tensor");
+    s.keep[i] = *t;
+    call.use(*t);
+  }
+  s.t.numel = s.rows * s.cols;
+  s.t.double_quant = truth(dq.p) ? 1 : 0;
+  s.t.packed = static_cast<uint8_t*>(ptr(s.keep[0]));
+  s.t.absmax = ptr(s.keep[1]);
+  s.t.nested_absmax = f32(s.keep[2]);
+  s.t.offset = f32(s.keep[3]);
+  return s;
+}
+
+// The frozen weight of a call: an Nf4Tensor, or [N, K] in 16 bits.
+struct Weight {
+  Stored stored;
+  Tensor w16;
+  bool is_stored = false;
+  const nf4_tensor* nf4() const { return is_stored ? &stored.t : nullptr; }
+};
+Weight weight_arg(Call& call, PyObject* o, int64_t N, int64_t K, at::ScalarType type) {   // N < 0: any
+  Weight w;
+  w.is_stored = PyObject_TypeCheck(o, reinterpret_cast<PyTypeObject*>(g_nf4_tensor));
+  if (w.is_stored) {
+    w.stored = stored_arg(call, o);
+    if ((N >= 0 && w.stored.rows != N) || w.stored.cols != K)
+      refuse(PyExc_ValueError, call.where() + "W has shape " + shape_text({w.stored.rows, w.stored.cols}) + ", expected " +
+                                   shape_text({N >= 0 ? N : w.stored.rows, K}));
+  } else {
+    const Tensor* t = tensor_of(o);
+    if (t == nullptr || t->dim() != 2) refuse(PyExc_ValueError, call.where() + "W must be an Nf4Tensor or a 2-D tensor");
+    w.w16 = call.read("W", o, {N >= 0 ? N : t->size(0), K}, type);
+  }
+  return w;
+}
+
+using Args = PyObject* const*;
+
+PyObject* rms_norm_fwd(Args a) {   // x, weight, eps, residual, checkpoint, y, h, rstd, stream
+  const char* name = "qlora_rms_norm_fwd";
+  const Tensor& given = matrix(name, "x", a[0]);
+  Call call(name, given, a[8]);
+  const int64_t M = given.size(0), K = given.size(1);
+  const at::ScalarType dt = given.scalar_type();
+  const nf4_dtype code = dtype_code(dt);
+  const Tensor x = call.read("x", a[0], {M, K}, dt);
+  const Tensor residual = call.read_or_none("residual", a[3], {M, K}, dt);
+  const Tensor weight = call.read("weight", a[1], {K}, at::kFloat);
+  const Tensor y = call.written("y", a[5], {M, K}, dt), rstd = call.written("rstd", a[7], {M}, at::kFloat);
+  const bool keep_h = residual.defined() || a[6] != Py_None;
+  const Tensor h = keep_h ? call.written("h", a[6], {M, K}, dt) : Tensor();
+  Act8 ck;
+  const bool made = a[4] == Py_True, checkpoint = made || (a[4] != Py_None && a[4] != Py_False);
+  if (checkpoint) ck = made ? act8_new(call, M, K) : act8_arg(call, a[4], M, K, true);
+  const qlora_act8 c = checkpoint ? ck.c() : qlora_act8{};
+  call.done(qlora_rms_norm_fwd(M, K, static_cast<float>(number(a[2])), code, ptr(x), ptr(residual), f32(weight), ptr(y),
+                               ptr(h), f32(rstd), checkpoint ? &c : nullptr, call.stream()));
+  return pack({wrap(y), keep_h ? wrap(h) : same(a[0]), wrap(rstd),
+               made ? wrap(ck) : checkpoint ? same(a[4]) : same(Py_None)});
+}
+
+PyObject* rms_norm_bwd(Args a) {   // dy, saved, rstd, weight, dresidual, dweight, dx, workspace, stream
+  const char* name = "qlora_rms_norm_bwd";
+  const Tensor& given = matrix(name, "dy", a[0]);
+  Call call(name, given, a[8]);
+  const int64_t M = given.size(0), K = given.size(1);
+  const at::ScalarType dt = given.scalar_type();
+  const nf4_dtype code = dtype_code(dt);
+  const Tensor dy = call.read("dy", a[0], {M, K}, dt);
+  const bool from_act8 = is_act8(a[1]);
+  const Act8 ck = from_act8 ? act8_arg(call, a[1], M, K, false) : Act8{};
+  const Tensor h = from_act8 ? Tensor() : call.read("h", a[1], {M, K}, dt);
+  const Tensor rstd = call.read("rstd", a[2], {M}, at::kFloat), weight = call.read("weight", a[3], {K}, at::kFloat);
+  const Tensor dres = call.read_or_none("dresidual", a[4], {M, K}, dt);
+  const Tensor dx = call.written("dx", a[6], {M, K}, dt);
+  Tensor dw, ws;
+  if (a[5] != Py_None && a[5] != Py_False) {
+    dw = call.written("dweight", a[5] == Py_True ? Py_None : a[5], {K}, at::kFloat);
+    ws = call.workspace(a[7], a[7] == Py_None ? qlora_rms_norm_bwd_workspace_bytes(M, K) : 0);
+  }
+  const qlora_act8 c = from_act8 ? ck.c() : qlora_act8{};
+  call.done(qlora_rms_norm_bwd(M, K, code, ptr(dy), ptr(h), from_act8 ? &c : nullptr, f32(rstd), f32(weight), ptr(dres),
+                               ptr(dx), f32(dw), ptr(ws), ws.defined() ? ws.numel() : 0, call.stream()));
+  return pack({wrap(dx), wrap(dw)});
+}
+
+PyObject* act8_quantize(Args a) {   // x, out, stream
+  const char* name = "qlora_act8_quantize";
+  const Tensor& given = matrix(name, "x", a[0]);
+  Call call(name, given, a[2]);
+  const int64_t M = given.size(0), K = given.size(1);
+  const nf4_dtype code = dtype_code(given.scalar_type());
+  const Tensor x = call.read("x", a[0], {M, K}, given.scalar_type());
+  const Act8 out = a[1] == Py_None ? act8_new(call, M, K) : act8_arg(call, a[1], M, K, true);
+  const qlora_act8 c = out.c();
+  call.done(qlora_act8_quantize(ptr(x), code, &c, call.stream()));
+  return a[1] == Py_None ? wrap(out) : same(a[1]);
+}
+
+// The codes of a checkpoint argument: the call's device and sizes.
+Tensor codes_of(const char* name, PyObject* o) {
+  if (!is_act8(o)) refuse(PyExc_ValueError, std::string(name) + ": an Act8 expected");
+  OwnedRef codes(PyObject_GetAttrString(o, "codes"));
+  return matrix(name, "codes", codes.p);
+}
+
+PyObject* act8_dequantize(Args a) {   // c, dtype, weight, out, stream
+  const char* name = "qlora_act8_dequantize";
+  const Tensor codes = codes_of(name, a[0]);
+  Call call(name, codes, a[4]);
+  const int64_t M = codes.size(0), K = codes.size(1);
+  const Act8 in = act8_arg(call, a[0], M, K, false);
+  const Tensor weight = call.read_or_none("weight", a[2], {K}, at::kFloat);
+  if (a[3] == Py_None && !THPDtype_Check(a[1])) refuse(PyExc_TypeError, call.where() + "a torch.dtype expected");
+  const at::ScalarType dt =
+      a[3] == Py_None ? reinterpret_cast<THPDtype*>(a[1])->scalar_type : call.type_of(a[3], "out");
+  const nf4_dtype code = dtype_code(dt);
+  const Tensor y = call.written("out", a[3], {M, K}, dt);
+  const qlora_act8 c = in.c();
+  call.done(qlora_act8_dequantize(&c, f32(weight), ptr(y), code, call.stream()));
+  return wrap(y);
+}
+
+PyObject* act8_grad_a(Args a) {   // G, c, alpha, mode, weight, dA, workspace, stream
+  const char* name = "qlora_act8_grad_a";
+  const Tensor& given = matrix(name, "G", a[0]);
+  const int64_t r = given.size(1);
+  const Tensor codes = codes_of(name, a[1]);
+  Call call(name, given, a[7]);
+  const int64_t M = codes.size(0), K = codes.size(1);
+  const Tensor G = call.read("G", a[0], {M, r}, at::kFloat);
+  const Act8 x = act8_arg(call, a[1], M, K, false);
+  const Tensor weight = call.read_or_none("weight", a[4], {K}, at::kFloat);
+  const Tensor dA = call.written("dA", a[5], {r, K}, at::kFloat);
+  const Tensor ws =
+      call.workspace(a[6], a[6] == Py_None ? qlora_act8_grad_a_workspace_bytes(M, K, static_cast<int32_t>(r)) : 0);
+  const qlora_act8 c = x.c();
+  call.done(qlora_act8_grad_a(static_cast<int32_t>(r), static_cast<float>(number(a[2])),
+                              static_cast<qlora_scale_mode>(whole(a[3])), f32(G), &c, f32(weight), f32(dA), ptr(ws),
+                              ws.numel(), call.stream()));
+  return wrap(dA);
+}
+
+PyObject* linear_bwd_act8(Args a) {   // dy, c, T, W, A, B, alpha, mode, weight, dx, dA, dB, workspace, stream
+  const char* name = "qlora_linear_bwd_act8";
+  const Tensor& given = matrix(name, "dy", a[0]);
+  const Tensor& ga = matrix(name, "A", a[4]);
+  Call call(name, given, a[13]);
+  const int64_t M = given.size(0), N = given.size(1), r = ga.size(0), K = ga.size(1);
+  const at::ScalarType dt = given.scalar_type();
+  const nf4_dtype code = dtype_code(dt);
+  const Tensor dy = call.read("dy", a[0], {M, N}, dt);
+  const Act8 x = act8_arg(call, a[1], M, K, false);
+  const Tensor weight = call.read_or_none("weight", a[8], {K}, at::kFloat);
+  const Tensor T = call.read("T", a[2], {M, r}, at::kFloat), A = call.read("A", a[4], {r, K}, at::kFloat),
+               B = call.read("B", a[5], {N, r}, at::kFloat);
+  const Weight W = weight_arg(call, a[3], N, K, dt);
+  const Tensor dx = call.written("dx", a[9], {M, K}, dt), dA = call.written("dA", a[10], {r, K}, at::kFloat),
+               dB = call.written("dB", a[11], {N, r}, at::kFloat);
+  const int32_t rank = static_cast<int32_t>(r);
+  const Tensor ws = call.workspace(
+      a[12], a[12] == Py_None ? qlora_bwd_act8_workspace_bytes(M, N, K, rank, code, W.is_stored ? 0 : 1) : 0);
+  const qlora_act8 c = x.c();
+  call.done(qlora_linear_bwd_act8(M, N, K, rank, static_cast<float>(number(a[6])),
+                                  static_cast<qlora_scale_mode>(whole(a[7])), code, ptr(dy), &c, f32(weight), f32(T),
+                                  W.nf4(), ptr(W.w16), f32(A), f32(B), ptr(dx), f32(dA), f32(dB), ptr(ws), ws.numel(),
+                                  call.stream()));
+  return pack({wrap(dx), wrap(dA), wrap(dB)});
+}
+
+PyObject* lm_loss(Args a) {   // x, W, targets, grad_scale, ignore_index, need_dx, loss, lse, dx, workspace, stream
+  const char* name = "qlora_lm_loss";
+  const Tensor& given = matrix(name, "x", a[0]);
+  Call call(name, given, a[10]);
+  const int64_t M = given.size(0), D = given.size(1);
+  const at::ScalarType dt = given.scalar_type();
+  const nf4_dtype code = dtype_code(dt);
+  const Tensor x = call.read("x", a[0], {M, D}, dt);
+  const Weight W = weight_arg(call, a[1], -1, D, dt);
+  const int64_t V = W.is_stored ? W.stored.rows : W.w16.size(0);
+  const Tensor targets = call.read("targets", a[2], {M}, at::kLong);
+  Tensor gs;
+  if (a[3] != Py_None) {
+    const Tensor* g = tensor_of(a[3]);
+    if (g == nullptr) refuse(PyExc_ValueError, call.where() + "grad_scale must be a tensor");
+    if (g->dim() == 0) {   // one value
+      OwnedRef flat(THPVariable_Wrap(g->reshape({1})));
+      gs = call.read("grad_scale", flat.p, {1}, at::kFloat);
+    } else {
+      gs = call.read("grad_scale", a[3], {g->numel() == 1 ? 1 : M}, at::kFloat);
+    }
+  }
+  const bool need_dx = truth(a[5]);
+  const Tensor loss = call.written("loss", a[6], {M}, at::kFloat), lse = call.written("lse", a[7], {M}, at::kFloat);
+  const Tensor dx = need_dx ? call.written("dx", a[8], {M, D}, dt) : Tensor();
+  const Tensor ws = call.workspace(
+      a[9], a[9] == Py_None ? qlora_lm_loss_workspace_bytes(M, V, D, W.is_stored ? 1 : 0, need_dx ? 1 : 0) : 0);
+  call.done(qlora_lm_loss(M, V, D, code, ptr(x), W.nf4(), ptr(W.w16),
+                          static_cast<const int64_t*>(targets.data_ptr()), whole(a[4]), f32(gs),
+                          gs.defined() && gs.numel() != 1 ? 1 : 0, f32(loss), f32(lse), ptr(dx), ptr(ws), ws.numel(),
+                          call.stream()));
+  return pack({wrap(loss), wrap(lse), wrap(dx)});
+}
+
+// One entry of the method table: the count of arguments, and C++ exceptions as Python's.
+template <PyObject* (*kOp)(Args), Py_ssize_t kCount>
+PyObject* entry(PyObject*, Args args, Py_ssize_t n) {
+  if (n != kCount) {
+    PyErr_Format(PyExc_TypeError, "%zd arguments expected, got %zd", kCount, n);
+    return nullptr;
+  }
+  try {
+    return kOp(args);
+  } catch (const PyError&) {
+  } catch (const std::exception& e) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+// init(Nf4Error, Act8, Nf4Tensor): the classes of binding.py.
+PyObject* init(PyObject*, Args args, Py_ssize_t n) {
+  if (n != 3) {
+    PyErr_SetString(PyExc_TypeError, "init(Nf4Error, Act8, Nf4Tensor)");
+    return nullptr;
+  }
+  g_nf4_error = same(args[0]);
+  g_act8 = same(args[1]);
+  g_nf4_tensor = same(args[2]);
+  Py_RETURN_NONE;
+}
+
+#define QLORA_ENTRY(op, count) \
+  {#op, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<op, count>)), METH_FASTCALL, nullptr}
+
+PyMethodDef g_methods[] = {
+    {"init", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&init)), METH_FASTCALL, nullptr},
+    QLORA_ENTRY(rms_norm_fwd, 9),
+    QLORA_ENTRY(rms_norm_bwd, 9),
+    QLORA_ENTRY(act8_quantize, 3),
+    QLORA_ENTRY(act8_dequantize, 5),
+    QLORA_ENTRY(act8_grad_a, 8),
+    QLORA_ENTRY(linear_bwd_act8, 14),
+    QLORA_ENTRY(lm_loss, 11),
+    {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_ops", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__torch_ops() { return PyModule_Create(&g_module); }
