@@ -778,6 +778,8 @@ int grad_slices(int64_t tiles, int64_t cols) {
 struct LmLayout {
   int64_t Mb, cols;
   int pieces, tiles, slices, piece_tiles;
+  bool stream;              // the logits come from lm_stream.cu
+  int parts, piece_parts;   // sums a token has, in all and from one piece
   size_t clean, zt, refs, spike, flags, part_sum, part_max, wy, wb, P, acc, total;
   LmLayout(int64_t M, int64_t V, int64_t D, bool stored, bool grad) {
     Mb = std::min(M, kBlockTokens);
@@ -786,6 +788,9 @@ struct LmLayout {
     pieces = static_cast<int>((V + cols - 1) / cols);
     piece_tiles = static_cast<int>(cols / kTile);
     tiles = static_cast<int>((V + kTile - 1) / kTile);
+    stream = Mb <= kLmStreamMaxM && D <= kLmStreamMaxD;
+    piece_parts = stream ? lm_stream_ctas() : 2 * piece_tiles;
+    parts = stream ? pieces * piece_parts : 2 * tiles;
     const int64_t tt = (Mb + kTile - 1) / kTile, ft = (D + kTile - 1) / kTile;
     slices = grad ? grad_slices(tt * ft, V - (pieces - 1) * cols) : 0;   // the last piece is the smallest
     size_t off = 0;
@@ -800,8 +805,8 @@ struct LmLayout {
     refs = take(grad ? 4 * m * (pieces + 1) : 0);
     spike = take(grad ? 4 * m * pieces : 0);
     flags = take(grad ? sizeof(int) * static_cast<size_t>(tt) * pieces : 0);
-    part_sum = take(4 * m * 2 * tiles);
-    part_max = take(grad ? 0 : 4 * m * 2 * tiles);
+    part_sum = take(4 * m * parts);
+    part_max = take(grad ? 0 : 4 * m * parts);
     wy = take(stored ? 2 * (m + kSamples) * D : 0);
     wb = take(stored ? 2 * static_cast<size_t>(std::min(cols, V)) * D : 0);
     P = take(grad ? 2 * m * cols : 0);
@@ -913,19 +918,41 @@ cudaError_t lm_loss(const LmLossArgs& a, void* ws, int* status, cudaStream_t st)
       p.range = a.f16 ? kRangeF16 : kRangeBf16;
       p.targets = clean;
       p.status = status;
-      p.part_sum = part_sum + static_cast<int64_t>(c) * 2 * L.piece_tiles * M;
-      if (!grad) {
-        p.part_max = part_max + static_cast<int64_t>(c) * 2 * L.piece_tiles * M;
-        if ((e = launch_lm_gemm<kMax>(p, xm, wm, pm, st)) != cudaSuccess) return e;
-        continue;
-      }
+      p.part_sum = part_sum + static_cast<int64_t>(c) * L.piece_parts * M;
+      p.part_max = part_max + static_cast<int64_t>(c) * L.piece_parts * M;
       p.ref = refs + static_cast<int64_t>(c) * M;
       p.ref_next = refs + static_cast<int64_t>(c + 1) * M;
       p.spike = spike + static_cast<int64_t>(c) * M;
       p.flags = flags + static_cast<int64_t>(c) * tt;
-      if ((e = launch_lm_gemm<kScores>(p, xm, wm, pm, st)) != cudaSuccess) return e;
-      p.redo = 1;
-      if ((e = launch_lm_gemm<kScores>(p, xm, wm, pm, st)) != cudaSuccess) return e;
+      if (L.stream) {
+        LmStreamArgs q{};
+        q.M = static_cast<int>(M);
+        q.D = a.D;
+        q.cols = cols;
+        q.v0 = v0;
+        q.x = x;
+        q.W = wc;
+        q.targets = clean;
+        q.range = p.range;
+        q.ref = p.ref;
+        q.ref_next = p.ref_next;
+        q.spike = p.spike;
+        q.flags = p.flags;
+        q.P = w + L.P;
+        q.ldp = L.cols;
+        q.part_sum = p.part_sum;
+        q.part_max = p.part_max;
+        if ((e = launch_lm_stream(q, grad, a.f16, st)) != cudaSuccess) return e;
+        q.redo = 1;
+        if (grad && (e = launch_lm_stream(q, true, a.f16, st)) != cudaSuccess) return e;
+      } else if (!grad) {
+        if ((e = launch_lm_gemm<kMax>(p, xm, wm, pm, st)) != cudaSuccess) return e;
+      } else {
+        if ((e = launch_lm_gemm<kScores>(p, xm, wm, pm, st)) != cudaSuccess) return e;
+        p.redo = 1;
+        if ((e = launch_lm_gemm<kScores>(p, xm, wm, pm, st)) != cudaSuccess) return e;
+      }
+      if (!grad) continue;
       LmParams g = p;
       g.red_len = cols;
       g.red_steps = static_cast<int>((cols + kStepK - 1) / kStepK);
@@ -942,8 +969,8 @@ cudaError_t lm_loss(const LmLossArgs& a, void* ws, int* status, cudaStream_t st)
     f.part_sum = part_sum;
     f.part_max = grad ? nullptr : part_max;
     f.refs = refs;
-    f.parts = 2 * L.tiles;
-    f.piece_parts = 2 * L.piece_tiles;
+    f.parts = L.parts;
+    f.piece_parts = L.piece_parts;
     f.pieces = L.pieces;
     f.zt = zt;
     f.clean = clean;

@@ -20,6 +20,30 @@ struct LmLossArgs {
   void* dx;                 // [M, D] or nullptr: no gradient
 };
 
+// lm_stream.cu: the logits of one piece of the vocabulary for at most kLmStreamMaxM tokens and
+// kLmStreamMaxD hidden elements; lm_stream_ctas() CTAs, each leaving its part of every token.
+constexpr int kLmStreamMaxM = 8;
+constexpr int kLmStreamMaxD = 4096;
+struct LmStreamArgs {
+  int M;
+  int64_t D, cols, v0;      // cols entries from v0 on
+  const void* x;            // [M, D]
+  const void* W;            // [cols, D]
+  const int64_t* targets;   // the target, or -1 for a token that does not count
+  int redo;                 // scores: nothing but ref_next unless flags[0] is set, then with the raised R
+  float range;
+  const float* ref;         // [M] R, times log2(e)
+  float* ref_next;
+  float* spike;
+  int* flags;
+  void* P;                  // scores: [M][ldp]
+  int64_t ldp;
+  float* part_sum;          // [CTA][M]
+  float* part_max;          // [CTA][M], times log2(e); without scores
+};
+int lm_stream_ctas();
+cudaError_t launch_lm_stream(const LmStreamArgs& a, bool scores, bool f16, cudaStream_t st);
+
 // stored: the head is given as NF4; grad: dx is asked for.
 size_t lm_loss_ws_bytes(int64_t M, int64_t V, int64_t D, bool stored, bool grad);
 cudaError_t lm_loss(const LmLossArgs& a, void* ws, int* status, cudaStream_t st);

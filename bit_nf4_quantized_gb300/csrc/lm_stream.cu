@@ -1,0 +1,220 @@
+// The loss's logits for at most 8 tokens: a pass over W at the speed of its bytes.
+//
+// With so few tokens the 256-row tensor-core tiles of lm_loss.cu are almost empty and their
+// 128-byte-wide boxes make poor use of DRAM (one token, 128256 x 4096: 280 us for 1.05 GB).
+// Here a CTA's 8 warps take 16 vocabulary rows at a time, each warp an eighth of the hidden
+// size, with W as the 16-row operand of m16n8k16 products and the tokens as the 8 columns.  A
+// lane reads 16 bytes of two rows straight into A fragments; the tokens stay in shared memory for
+// the whole launch.  (The order of the contraction inside 32 elements is the same permutation for
+// both operands.)  Sums leave the tensor cores,
+// which truncate, every 128 elements and go on in fp32 registers.  The warps' parts of a row
+// meet in shared memory; the next rows' loads are under way meanwhile.
+//
+// Outputs as lm_loss.cu's: exponentials relative to R as 16-bit P with their sums, or without a
+// gradient each CTA's running maximum and sum.
+#include <mutex>
+
+#include "lm_loss.cuh"
+#include "mma_sync.cuh"
+
+namespace qnf4 {
+namespace {
+
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kRows = 16;                      // vocabulary rows of a tile
+constexpr int kBatch = 4;                      // 32-deep steps between fp32 additions
+constexpr int kSteps = 16;                     // of a warp at most: hidden sizes up to 4096
+constexpr float kLog2e = 1.4426950408889634f;
+static_assert(kWarps * kSteps * 32 == kLmStreamMaxD, "a warp's steps cover the hidden size");
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void atomic_max_float(float* a, float v) {   // never NaN
+  if (v >= 0.0f) atomicMax(reinterpret_cast<int*>(a), __float_as_int(v));
+  else atomicMin(reinterpret_cast<unsigned*>(a), __float_as_uint(v));
+}
+
+// kScores: P and sums relative to R; else running maxima and sums.
+template <bool kScores, bool kF16>
+__global__ void __launch_bounds__(kThreads, 2) lm_stream(const LmStreamArgs p) {
+  extern __shared__ uint4 xs[];
+  __shared__ float part[2][kWarps][kRows][kLmStreamMaxM];
+  __shared__ float ends[kWarps][2][32];
+  pdl_allow_next();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (kScores && p.redo) {
+    if (blockIdx.x == 0 && threadIdx.x < p.M) p.ref_next[threadIdx.x] = fmaxf(p.ref[threadIdx.x], p.spike[threadIdx.x]);
+    if (p.flags[0] == 0) return;
+  }
+  const int g = lane >> 2, c = lane & 3;
+  const int steps = static_cast<int>((p.D + 32 * kWarps - 1) / (32 * kWarps));
+  const int k0 = warp * steps * 32 + 8 * c;            // this lane's first element
+  // the tokens and a row of zeros, `pitch` 16-byte pieces a row: an odd multiple of 64 bytes, so that
+  // two rows' 64 bytes lie on different banks
+  const int depth = steps * kWarps * 4, pitch = depth + 4;
+  for (int i = threadIdx.x; i < (p.M + 1) * depth; i += kThreads) {
+    const int row = i / depth, piece = i - row * depth;
+    xs[row * pitch + piece] = row < p.M && piece * 8 < p.D
+                                  ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.D + piece * 8)
+                                  : make_uint4(0, 0, 0, 0);
+  }
+  __syncthreads();
+  const uint4* xr = xs + min(g, p.M) * pitch + warp * steps * 4 + c;
+  // this lane's values of a finished tile: token lane % 8, rows 4 (lane / 8) ..
+  const int tok = lane & 7, r0 = (lane >> 3) * 4;
+  const bool in = tok < p.M;
+  const int64_t y = in ? p.targets[tok] : -1;
+  const bool live = y >= 0;
+  float r2 = kScores && in ? p.ref[tok] : 0.0f;
+  if (kScores && p.redo && in) r2 = fmaxf(r2, p.spike[tok]);
+  float mx = -INFINITY, sum = 0.0f;
+
+  const int64_t tiles = (p.cols + kRows - 1) / kRows;
+  const uint16_t* W = static_cast<const uint16_t*>(p.W);
+  auto row_of = [&](int64_t tile, int h) { return W + min(tile * kRows + g + 8 * h, p.cols - 1) * p.D; };
+  auto load = [&](const uint16_t* a, const uint16_t* b, int batch, uint4 (&w)[kBatch][2]) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (batch * kBatch + i >= steps) break;    // another warp's elements follow
+      // past the hidden size the tokens' values are zero: any address of the row will do
+      const int k = min(k0 + 32 * (batch * kBatch + i), static_cast<int>(p.D) - 8);
+      w[i][0] = __ldcs(reinterpret_cast<const uint4*>(a + k));
+      w[i][1] = __ldcs(reinterpret_cast<const uint4*>(b + k));
+    }
+  };
+  const int batches = (steps + kBatch - 1) / kBatch;
+  int64_t tile = blockIdx.x;
+  uint4 w[kBatch][2];
+  if (tile < tiles) load(row_of(tile, 0), row_of(tile, 1), 0, w);
+  int turn = 0;
+  for (; tile < tiles; tile += gridDim.x, turn ^= 1) {
+    const uint16_t* a = row_of(tile, 0);
+    const uint16_t* b = row_of(tile, 1);
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int q = 0; q < batches; ++q) {
+      {
+        uint4 now[kBatch][2];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) now[i][0] = w[i][0], now[i][1] = w[i][1];
+        if (q + 1 < batches) load(a, b, q + 1, w);
+        else if (tile + gridDim.x < tiles) load(row_of(tile + gridDim.x, 0), row_of(tile + gridDim.x, 1), 0, w);
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (q * kBatch + i >= steps) break;
+          const uint4 x = xr[(q * kBatch + i) * 4];
+          mma16816<kF16>(d, now[i][0].x, now[i][1].x, now[i][0].y, now[i][1].y, x.x, x.y);
+          mma16816<kF16>(d, now[i][0].z, now[i][1].z, now[i][0].w, now[i][1].w, x.z, x.w);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] += d[j];
+      }
+    }
+    *reinterpret_cast<float2*>(&part[turn][warp][g][2 * c]) = make_float2(acc[0], acc[1]);
+    *reinterpret_cast<float2*>(&part[turn][warp][g + 8][2 * c]) = make_float2(acc[2], acc[3]);
+    __syncthreads();
+    // one warp finishes the tile while the others go on (its buffer is written again after the
+    // next barrier)
+    if (warp == static_cast<int>((tile / gridDim.x) % kWarps)) {
+      float z[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        z[j] = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) z[j] += part[turn][q][r0 + j][tok];
+        const int64_t v = tile * kRows + r0 + j;
+        if (v >= p.cols || p.v0 + v == y) z[j] = -INFINITY;     // no entry, or the target's own
+      }
+      if (kScores) {
+        float e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          mx = fmaxf(mx, z[j]);
+          e[j] = live ? ex2(fmaf(z[j], kLog2e, -r2)) : 0.0f;
+          sum += e[j];
+        }
+        if (in) {   // rows of P are padded to whole tiles of 256
+          uint2 o;
+          if (kF16) {
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o.x) : "f"(e[1]), "f"(e[0]));
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o.y) : "f"(e[3]), "f"(e[2]));
+          } else {
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.x) : "f"(e[1]), "f"(e[0]));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.y) : "f"(e[3]), "f"(e[2]));
+          }
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.P) + tok * p.ldp + tile * kRows + r0) = o;
+        }
+      } else {
+        const float top = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) * kLog2e;
+        // NaN stays in the sum: a maximum ignores it, an exponential does not
+        const float m2 = fmaxf(mx, top), base = m2 == -INFINITY ? 0.0f : m2;
+        sum = sum * (mx == m2 ? 1.0f : ex2(mx - base));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum += ex2(fmaf(z[j], kLog2e, -base));
+        mx = m2;
+      }
+    }
+  }
+  // P's columns up to the next 64 after the piece's last tile hold zeros
+  if (kScores && blockIdx.x == 0 && in && warp == 0) {
+    for (int64_t v = tiles * kRows + lane / 8; v < (p.cols + 63) / 64 * 64; v += 4)
+      static_cast<uint16_t*>(p.P)[tok * p.ldp + v] = 0;
+  }
+  // the CTA's maximum and sum of each token
+  ends[warp][0][lane] = mx;
+  ends[warp][1][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && lane < p.M) {
+    float m = -INFINITY, s = 0.0f;
+    for (int q = 0; q < kWarps; ++q)
+      for (int h = 0; h < 4; ++h) m = fmaxf(m, ends[q][0][lane + 8 * h]);
+    for (int q = 0; q < kWarps; ++q)
+      for (int h = 0; h < 4; ++h) {
+        const float v = ends[q][1][lane + 8 * h], mq = ends[q][0][lane + 8 * h];
+        s += kScores || mq == m ? v : v == 0.0f ? 0.0f : v * exp2f(mq - m);
+      }
+    p.part_sum[static_cast<int64_t>(blockIdx.x) * p.M + lane] = s;
+    if (kScores) {
+      const float m2 = m * kLog2e;
+      if (live && !p.redo && m2 > r2 + p.range) {
+        atomic_max_float(p.spike + lane, m2);
+        p.flags[0] = 1;
+      }
+    } else {
+      p.part_max[static_cast<int64_t>(blockIdx.x) * p.M + lane] = m;
+    }
+  }
+}
+
+}  // namespace
+
+int lm_stream_ctas() { return 2 * device_sm_count(); }
+
+cudaError_t launch_lm_stream(const LmStreamArgs& a, bool scores, bool f16, cudaStream_t st) {
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  const int steps = static_cast<int>((a.D + 32 * kWarps - 1) / (32 * kWarps));
+  const size_t smem = static_cast<size_t>(a.M + 1) * (steps * kWarps * 4 + 4) * sizeof(uint4);
+  std::call_once(once, [&] {
+    const int most = (kLmStreamMaxM + 1) * (kSteps * kWarps * 4 + 4) * static_cast<int>(sizeof(uint4));
+    for (const void* k : {reinterpret_cast<const void*>(lm_stream<true, true>), reinterpret_cast<const void*>(lm_stream<true, false>),
+                          reinterpret_cast<const void*>(lm_stream<false, true>), reinterpret_cast<const void*>(lm_stream<false, false>)})
+      if (err == cudaSuccess) err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  });
+  if (err != cudaSuccess) return err;
+  note_launch();
+  const dim3 grid(static_cast<unsigned>(lm_stream_ctas())), block(kThreads);
+  if (scores)
+    return f16 ? launch_pdl(lm_stream<true, true>, grid, block, smem, st, 1, a)
+               : launch_pdl(lm_stream<true, false>, grid, block, smem, st, 1, a);
+  return f16 ? launch_pdl(lm_stream<false, true>, grid, block, smem, st, 1, a)
+             : launch_pdl(lm_stream<false, false>, grid, block, smem, st, 1, a);
+}
+
+}  // namespace qnf4

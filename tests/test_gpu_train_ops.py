@@ -322,7 +322,9 @@ def _check_loss(x, W, t, g, dtype, loss, lse, dx, ref=None):
 
 
 LOSS_SIZES = [(1, 1, 64), (1, 300, 64), (2, 2, 72), (3, 257, 64), (17, 256, 576), (130, 1000, 200), (257, 513, 576),
-              (300, 5000, 136), (64, 12001, 1000), (600, 300, 1096)]
+              (300, 5000, 136), (64, 12001, 1000), (600, 300, 1096),
+              # few tokens: the pass over the vocabulary's bytes, its limits and just past them
+              (8, 1000, 4096), (5, 333, 1000), (1, 5000, 2048), (8, 40, 64), (4, 700, 4104), (9, 700, 576)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
@@ -366,18 +368,19 @@ def test_loss_of_a_stored_head(lib, dtype, dq, M, V, D):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("above", [5.0, 30.0, 70.0, 200.0])
-def test_loss_spikes_far_above_the_target(lib, dtype, above):
+@pytest.mark.parametrize("M", [600, 8])
+def test_loss_spikes_far_above_the_target(lib, dtype, above, M):
     """One vocabulary entry `above` the target's logit, for some tokens of some tiles."""
-    M, V, D = 600, 1500, 64
+    V, D = 1500, 64
     rng = _rng(11)
     W = rng.standard_normal((V, D)) * 0.05
     x = rng.standard_normal((M, D))
     W[:, 0], x[:, 0] = 0.0, 0.0
     spike = [700, 1400]
     W[spike, 0] = 1.0
-    x[5, 0] = x[300, 0] = x[599, 0] = above
+    x[5, 0] = x[M // 2, 0] = x[M - 1, 0] = above
     t = rng.integers(0, 256, M)
-    t[7] = -100
+    t[6] = -100
     W, x = _dev(W, DT[dtype]), _dev(x, DT[dtype])
     loss, lse, dx = b.qlora_lm_loss(x, W, torch.from_numpy(t).to(DEV))
     _check_loss(x, W, t, None, dtype, loss, lse, dx)
