@@ -5,6 +5,7 @@
 #include <type_traits>
 
 #include "mma_sync.cuh"
+#include "tc_ptx.cuh"
 #include "train_ops.cuh"
 
 namespace qnf4 {
@@ -125,7 +126,9 @@ cudaError_t dequantize_t(Act8View in, int64_t M, int64_t K, const float* weight,
 //
 // e belongs to the warp and falls when a step's largest |G scale| would leave half's range; the
 // sums then fall with it, and are put back into fp32's own scale at the end.  Tokens are cut in
-// slices, whose sums a second launch adds in order.
+// slices; the CTAs of up to 16 slices are a cluster, which adds its sums in order through
+// distributed shared memory.  Only where one cluster a column group leaves SMs idle are there
+// several, whose sums a second launch adds.
 constexpr int kGradRanks = 16;
 constexpr int kGradWarps = 4;                                  // one block of 128 features each
 constexpr int kGradThreads = kGradWarps * 32;
@@ -137,8 +140,9 @@ constexpr int kRingCodes = 16 * kCodePitch, kRingG = 16 * kGPitch * 4, kRingS = 
 constexpr int kRingBytes = kRingCodes + kRingG + kRingS;       // 10496
 constexpr int kRing = 5;
 constexpr int kGradSmem = kRing * kRingBytes;
-
-__device__ __forceinline__ uint32_t smem_at(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+constexpr int kSumPitch = kGradCols + 4;                       // floats
+constexpr int kClusterMax = 16;
+static_assert(kGradRanks * kSumPitch * 4 <= kGradSmem, "a CTA's sums take the ring's place");
 
 // 16 (or 4) bytes to shared memory, of which the last 16 - n (4 - n) are zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
@@ -167,19 +171,19 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 
 template <bool kVec>
 __global__ void __launch_bounds__(kGradThreads, kGradCtas)
-act8_grad(const ActGradArgs a, int slice_steps, int slices, float* part) {
+act8_grad(const ActGradArgs a, int slice_steps, int cluster, int clusters, float* part) {
   extern __shared__ __align__(16) uint8_t ring[];
   pdl_allow_next();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
   const int64_t nb = (a.K + kActBlock - 1) / kActBlock;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kGradCols, b0 = static_cast<int64_t>(blockIdx.x) * kGradWarps;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * kGradCols, b0 = static_cast<int64_t>(blockIdx.y) * kGradWarps;
   const int j0 = blockIdx.z * kGradRanks;
   const int64_t steps = (a.M + 15) / 16;
-  const int64_t s0 = blockIdx.y * static_cast<int64_t>(slice_steps), s1 = min(s0 + slice_steps, steps);
+  const int64_t s0 = min(blockIdx.x * static_cast<int64_t>(slice_steps), steps), s1 = min(s0 + slice_steps, steps);
   const int n_steps = static_cast<int>(s1 - s0);
-  const uint32_t ring0 = smem_at(ring);
+  const uint32_t ring0 = tc::smem_u32(ring);
   const int64_t bytes = a.M * a.K;
   const int64_t row_end = min(c0 + kGradCols, a.K);     // the features of this CTA's rows end here
 
@@ -321,34 +325,57 @@ act8_grad(const ActGradArgs a, int slice_steps, int slices, float* part) {
   }
   // acc[n][k]: rank g + 8 (k / 2), feature 32 q + 16 (k % 2) + n of the warp's block, times 2^e
   const float back = __int_as_float((127 - e) << 23);
-  const bool direct = slices == 1;
-  float* dst = direct ? a.dA : part + static_cast<int64_t>(blockIdx.y) * a.r * a.K;
+  const bool direct = clusters == 1;
+  float* dst = direct ? a.dA : part + static_cast<int64_t>(blockIdx.x / cluster) * a.r * a.K;
+  // four neighbouring features of one rank
+  auto store = [&](int rank, int64_t kk, float4 v) {
+    if (j0 + rank >= a.r || kk >= a.K) return;
+    float* row = dst + static_cast<int64_t>(j0 + rank) * a.K;
+    float w[4] = {v.x, v.y, v.z, v.w};
+    if (direct) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int rank = j0 + g + 8 * (k / 2);
-    if (rank >= a.r) continue;
-    float* row = dst + rank * a.K;
+      for (int i = 0; i < 4; ++i) w[i] = w[i] * a.s * (a.weight != nullptr && kk + i < a.K ? a.weight[kk + i] : 1.0f);
+    }
+    if (kVec) {
+      *reinterpret_cast<float4*>(row + kk) = make_float4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (kk + i < a.K) row[kk + i] = w[i];
+    }
+  };
+  float* sums = reinterpret_cast<float*>(ring);
+  __syncthreads();             // the ring's stages have been read
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
 #pragma unroll
     for (int n = 0; n < 16; n += 4) {
-      const int64_t kk = c0 + warp * kActBlock + 32 * q + 16 * (k % 2) + n;
-      float v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = acc[n + i][k] * back;
-        if (direct) v[i] = v[i] * a.s * (a.weight != nullptr && kk + i < a.K ? a.weight[kk + i] : 1.0f);
-      }
-      if (kVec) {
-        if (kk < a.K) *reinterpret_cast<float4*>(row + kk) = make_float4(v[0], v[1], v[2], v[3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (kk + i < a.K) row[kk + i] = v[i];
-      }
+      const int rank = g + 8 * (k / 2), col = warp * kActBlock + 32 * q + 16 * (k % 2) + n;
+      const float4 v = make_float4(acc[n][k] * back, acc[n + 1][k] * back, acc[n + 2][k] * back, acc[n + 3][k] * back);
+      if (cluster == 1) store(rank, c0 + col, v);
+      else *reinterpret_cast<float4*>(sums + rank * kSumPitch + col) = v;
     }
+  if (cluster == 1) return;
+  tc::cluster_sync();
+  for (int i = static_cast<int>(tc::cluster_ctarank()) * kGradThreads + threadIdx.x; i < kGradRanks * kGradCols / 4;
+       i += cluster * kGradThreads) {
+    const int rank = i / (kGradCols / 4), col = 4 * (i % (kGradCols / 4));
+    const uint32_t at = tc::smem_u32(sums + rank * kSumPitch + col);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int y = 0; y < cluster; ++y) {
+      float4 u;
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(u.x), "=f"(u.y), "=f"(u.z), "=f"(u.w)
+                   : "r"(tc::mapa_shared(at, static_cast<uint32_t>(y))));
+      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
+    store(rank, c0 + col, v);
   }
+  tc::cluster_sync();          // no CTA leaves while another reads its sums
 }
 
-// dA = s * weight * (the slices' sums in order), kW values a thread.
+// dA = s * weight * (the clusters' sums in order), kW values a thread.
 template <int kW>
 __global__ void act8_grad_finish(const ActGradArgs a, const float* part, int slices) {
   pdl_allow_next();
@@ -371,33 +398,45 @@ __global__ void act8_grad_finish(const ActGradArgs a, const float* part, int sli
   for (int k = 0; k < kW; ++k) a.dA[i + k] = v[k] * a.s * (a.weight != nullptr ? a.weight[kk + k] : 1.0f);
 }
 
-// Slices of the tokens: the count with the least time, in units of a quarter of a step: rounds of
-// resident CTAs times their steps and 4 steps' worth for a CTA's own ends, and with several
-// slices 6 steps for the launch that adds them and a quarter for reading each.
-int grad_slices(int64_t M, int64_t K, int r) {
+// Slices of the tokens, as clusters of CTAs: the counts with the least time, in units of a quarter
+// of a step: rounds of resident CTAs times their steps and 4 steps' worth for a CTA's own ends, 2
+// for a cluster's sums and one for every 8 CTAs of it, and with several clusters 10 for the launch
+// that adds them and a quarter for reading each.
+struct GradPlan {
+  int cluster, clusters;
+  int64_t per;      // steps of a slice
+};
+GradPlan grad_plan(int64_t M, int64_t K, int r) {
   const int64_t groups = (K + kGradCols - 1) / kGradCols * ((r + kGradRanks - 1) / kGradRanks);
   const int64_t steps = (M + 15) / 16, slots = kGradCtas * static_cast<int64_t>(device_sm_count());
-  int best = 1;
+  GradPlan best{1, 1, steps};
   int64_t best_cost = INT64_MAX;
-  for (int s = 1; s <= 64 && s <= steps; ++s) {
-    const int64_t per = (steps + s - 1) / s;
-    const int64_t rounds = (groups * s + slots - 1) / slots;
-    const int64_t cost = 4 * rounds * (per + 4) + (s > 1 ? 24 + s : 0);
-    if (cost < best_cost) best = s, best_cost = cost;
-  }
+  for (int n = 1; n <= 8; ++n)
+    for (int c = 1; c <= kClusterMax && n * c <= std::max<int64_t>(steps, 1); ++c) {
+      const int64_t per = (steps + n * c - 1) / (n * c);
+      const int64_t rounds = (groups * n * c + slots - 1) / slots;
+      // CTAs that share an SM share its issue slots: a lone one runs its steps about 2.5 times as fast
+      const int64_t sharing = std::min<int64_t>(kGradCtas, (groups * n * c + device_sm_count() - 1) / device_sm_count());
+      const int64_t cost = rounds * (per * (1 + sharing) * 4 / (1 + kGradCtas) + 16) + (c > 1 ? 8 + c / 2 : 0) + (n > 1 ? 40 + n : 0);
+      if (cost < best_cost) best = GradPlan{c, n, per}, best_cost = cost;
+    }
   return best;
 }
 
 template <bool kVec>
-cudaError_t launch_grad(const ActGradArgs& a, dim3 grid, int per, int slices, float* part, cudaStream_t st) {
+cudaError_t launch_grad(const ActGradArgs& a, const GradPlan& g, float* part, cudaStream_t st) {
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
   std::call_once(once, [&] {
     err = cudaFuncSetAttribute(act8_grad<kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(act8_grad<kVec>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   });
   if (err != cudaSuccess) return err;
   note_launch();
-  return launch_pdl(act8_grad<kVec>, grid, dim3(kGradThreads), kGradSmem, st, 1, a, per, slices, part);
+  const dim3 grid(static_cast<unsigned>(g.cluster * g.clusters), static_cast<unsigned>((a.K + kGradCols - 1) / kGradCols),
+                  static_cast<unsigned>((a.r + kGradRanks - 1) / kGradRanks));
+  return launch_pdl(act8_grad<kVec>, grid, dim3(kGradThreads), kGradSmem, st, static_cast<unsigned>(g.cluster), a,
+                    static_cast<int>(g.per), g.cluster, g.clusters, part);
 }
 
 }  // namespace
@@ -428,26 +467,23 @@ cudaError_t launch_act8_dequantize(Act8View in, int64_t M, int64_t K, const floa
 }
 
 size_t act8_grad_ws_bytes(int64_t M, int64_t K, int r) {
-  return M == 0 ? 0 : sizeof(float) * static_cast<size_t>(grad_slices(M, K, r)) * static_cast<size_t>(r) * K;
+  if (M == 0) return 0;
+  const GradPlan g = grad_plan(M, K, r);
+  return g.clusters == 1 ? 0 : sizeof(float) * static_cast<size_t>(g.clusters) * static_cast<size_t>(r) * K;
 }
 
 cudaError_t launch_act8_grad(const ActGradArgs& a, void* ws, cudaStream_t st) {
   if (a.M == 0) return cudaMemsetAsync(a.dA, 0, sizeof(float) * static_cast<size_t>(a.r) * a.K, st);
-  const int want = grad_slices(a.M, a.K, a.r);
-  const int64_t steps = (a.M + 15) / 16, per = (steps + want - 1) / want;
-  const int slices = static_cast<int>((steps + per - 1) / per);
-  const dim3 grid(static_cast<unsigned>((a.K + kGradCols - 1) / kGradCols), static_cast<unsigned>(slices),
-                  static_cast<unsigned>((a.r + kGradRanks - 1) / kGradRanks));
+  const GradPlan g = grad_plan(a.M, a.K, a.r);
   auto* part = static_cast<float*>(ws);
-  const cudaError_t e = a.K % 16 == 0 ? launch_grad<true>(a, grid, static_cast<int>(per), slices, part, st)
-                                      : launch_grad<false>(a, grid, static_cast<int>(per), slices, part, st);
-  if (e != cudaSuccess || slices == 1) return e;
+  const cudaError_t e = a.K % 16 == 0 ? launch_grad<true>(a, g, part, st) : launch_grad<false>(a, g, part, st);
+  if (e != cudaSuccess || g.clusters == 1) return e;
   const int w = a.K % 4 == 0 ? 4 : 1;
   const int64_t n = static_cast<int64_t>(a.r) * a.K / w;
-  const dim3 fgrid(static_cast<unsigned>((n + kThreads - 1) / kThreads));
+  const dim3 grid(static_cast<unsigned>((n + kThreads - 1) / kThreads));
   note_launch();
-  return w == 4 ? launch_pdl(act8_grad_finish<4>, fgrid, dim3(kThreads), 0, st, 1, a, static_cast<const float*>(part), slices)
-                : launch_pdl(act8_grad_finish<1>, fgrid, dim3(kThreads), 0, st, 1, a, static_cast<const float*>(part), slices);
+  return w == 4 ? launch_pdl(act8_grad_finish<4>, grid, dim3(kThreads), 0, st, 1, a, static_cast<const float*>(part), g.clusters)
+                : launch_pdl(act8_grad_finish<1>, grid, dim3(kThreads), 0, st, 1, a, static_cast<const float*>(part), g.clusters);
 }
 
 }  // namespace qnf4

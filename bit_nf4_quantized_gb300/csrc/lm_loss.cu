@@ -13,28 +13,25 @@
 //
 // R starts as the target's logit (for half, whose largest value is 65504, the largest of it and
 // of 8 other entries' logits).  Only range matters: a bf16 P holds exp(z - R) up to z - R = 88,
-// a half one up to 11.  A logit further above R than that is found when it is met: the row's
-// largest is recorded, and once the piece's logits are done, the token tiles with such a row take
-// them once more with the raised R; the sums taken so far are scaled by exp(R_old - R_new).  R
-// never exceeds the largest logit, so the largest term never vanishes.  Exponentials are powers
-// of two of z log2(e) - R2 with R2 the reference in those units: the rounding of R2 is common to
-// every term and cancels.
+// a half one up to 11.  A logit further above R than that is found by the pass that meets it,
+// which records the row's largest; the token tiles with such a row run that piece once more with
+// the raised R, and the sums taken so far are scaled by exp(R_old - R_new).  R never exceeds the
+// largest logit, so the largest term never vanishes.  Exponentials are powers of two of
+// z log2(e) - R2 with R2 the reference in those units: the rounding of R2 is common to every
+// term and cancels.
 //
 // Kernels.
-//   lm_prep       z[t][y], the tokens that count, R's start
-//   lm_gemm       one persistent launch over all pieces: clusters of two CTAs, 2-SM tcgen05.mma
-//                 on tiles of 256 x 256, fed by TMA, two accumulators in TMEM.
-//       scores    256 tokens x 256 entries: x as A (each token's logits in one TMEM lane, so a
-//                 thread owns a row), W as B, both K-major.  The epilogue takes exponentials, row
-//                 sums and P (16 bits, through a swizzled box and a TMA store), or, without a
-//                 gradient, each half tile's row maximum and sum.
-//       gradient  256 features x 256 tokens: A = W[piece] read MN-major, B = P; the contraction
-//                 (the piece) is split in `slices` parts with an fp32 sum each when there are too
-//                 few tiles for the SMs.
-//     A piece's gradient starts when every cluster has finished its scores: a counter in global
-//     memory that the clusters wait for, which needs them all resident, so the launch is
-//     cooperative.  The next piece's scores need no such wait (P has two buffers), so a cluster
-//     that has fewer gradient tiles goes on to more of the scores.
+//   lm_prep       z[t][y], the tokens that count, R's start (without a gradient, the epilogue warps
+//                 of the first launch, under its first tiles' products)
+//   lm_gemm<kScores / kMax>  clusters of two CTAs, persistent over tiles of 256 tokens x 256
+//                 vocabulary entries: 2-SM tcgen05.mma with x as A (each token's logits in one
+//                 TMEM lane, so a thread owns a row), W as B, both K-major through TMA.  The
+//                 epilogue takes exponentials, row sums and P (bf16 / half through a swizzled
+//                 shared-memory box and a TMA store), or, without a gradient, each half tile's
+//                 row maximum and sum.
+//   lm_gemm<kGrad>   tiles of 256 features x 256 tokens: A = W[piece] read MN-major, B = P;
+//                 the contraction (the piece) is split in `slices` parts with an fp32 sum each
+//                 when there are too few tiles for the SMs.
 //   lm_finish     each token's totals, loss and lse, and dx = a (sum of the slices) - b W[y],
 //                 rounded once to 16 bits
 //
@@ -44,7 +41,6 @@
 // Every mbarrier wait is bounded in time; one that gives up sets NF4_ERR_TIMEOUT in the status
 // word and the CTA winds down, freeing its TMEM.
 #include <algorithm>
-#include <atomic>
 
 #include <cuda_fp16.h>
 
@@ -76,7 +72,7 @@ constexpr int kBoxCols = 32;                // a warp's store box: 32 tokens x 3
 constexpr int kBoxBytes = 32 * kBoxCols * 2;
 constexpr int kBoxes = 2;                   // per epilogue warp
 constexpr int kBarFull = 0, kBarEmpty = kStages, kBarAccFull = 2 * kStages, kBarAccEmpty = kBarAccFull + 2,
-              kBarDone = kBarAccEmpty + 2, kBarPhase = kBarDone + 1, kBarAck = kBarPhase + 1, kNumBars = kBarAck + 1;
+              kBarDone = kBarAccEmpty + 2, kNumBars = kBarDone + 1;
 constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiWarps * kBoxes * kBoxBytes + kNumBars * 8 + 16;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
@@ -86,30 +82,127 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRangeBf16 = 86.0f, kRangeF16 = 15.9f;
 constexpr int kSamples = 8;                 // entries whose logits half's R starts from, beside the target
 
+__device__ __forceinline__ float lo16(uint32_t w, int f16) {
+  return f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(w & 0xffffu))) : __uint_as_float(w << 16);
+}
+__device__ __forceinline__ float hi16(uint32_t w, int f16) {
+  return f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16))) : __uint_as_float(w & 0xffff0000u);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// The target of a token, or -1 where it does not count.
+__device__ __forceinline__ int64_t clean_target(int64_t y, int64_t V, int64_t ignore) {
+  return y >= 0 && y < V && y != ignore ? y : -1;
+}
+// Entry i of the kSamples of a vocabulary.
+__device__ __forceinline__ int64_t sample_of(int i, int64_t V) { return V * i / kSamples; }
+
+__device__ __forceinline__ float dot8(uint4 u, uint4 v, int f16, float s) {
+  const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    s = fmaf(lo16(uu[k], f16), lo16(vv[k], f16), s);
+    s = fmaf(hi16(uu[k], f16), hi16(vv[k], f16), s);
+  }
+  return s;
+}
+
+struct PrepArgs {
+  int64_t M, V, D8, ignore;
+  const uint4* x;
+  const uint4* rows;        // W, or with by_token the decoded rows of the targets and then of the samples
+  int by_token, f16;
+  const int64_t* targets;
+  int64_t* clean;           // the target, or -1 for a token that does not count
+  float* zt;                // x[t] . W[y]
+  float* ref;               // R's start, times log2(e), or nullptr without a gradient
+  float* spike;             // [pieces][M]
+  int* flags;               // [pieces][tiles_t]
+  int pieces, tiles_t;
+};
+
+// What a pass needs to know of token t, by one warp or by the kWarps warps of a CTA (red: their parts):
+// its target's logit in fp32, R's start (kSample: the largest of it and the samples' logits), the
+// pieces' marks.  A target outside [0, V) that is not ignore_index sets NF4_ERR_ARG.
+template <bool kSample, int kWarps>
+__device__ __forceinline__ void prep_token(const PrepArgs& a, int64_t t, int thread, float (*red)[1 + kSamples],
+                                           int* status) {
+  constexpr int kDots = kSample ? 1 + kSamples : 1;
+  const int64_t given = a.targets[t], y = clean_target(given, a.V, a.ignore);
+  float s[kDots];
+#pragma unroll
+  for (int k = 0; k < kDots; ++k) s[k] = 0.0f;
+  if (y >= 0) {
+    const uint4* x = a.x + t * a.D8;
+    const uint4* w = a.rows + (a.by_token ? t : y) * a.D8;
+#pragma unroll 4
+    for (int64_t i = thread; i < a.D8; i += 32 * kWarps) {
+      const uint4 u = x[i];
+      s[0] = dot8(u, w[i], a.f16, s[0]);
+      if (kSample) {
+#pragma unroll
+        for (int k = 0; k < kDots - 1; ++k)
+          s[1 + k] = dot8(u, a.rows[(a.by_token ? a.M + k : sample_of(k, a.V)) * a.D8 + i], a.f16, s[1 + k]);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kDots; ++k) s[k] = warp_sum(s[k]);
+  if (kWarps > 1) {
+    if ((thread & 31) == 0)
+#pragma unroll
+      for (int k = 0; k < kDots; ++k) red[thread >> 5][k] = s[k];
+    __syncthreads();
+  }
+  if (thread == 0) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kDots; ++k) {
+#pragma unroll
+      for (int q = 1; q < kWarps; ++q) s[k] += red[q][k];
+      top = fmaxf(top, s[k]);
+    }
+    a.clean[t] = y;
+    a.zt[t] = s[0];
+    if (a.ref != nullptr) a.ref[t] = (kSample ? top : s[0]) * kLog2e;
+    if (y < 0 && given != a.ignore) atomicCAS(status, 0, static_cast<int>(NF4_ERR_ARG));
+  }
+  for (int c = thread; c < a.pieces; c += 32 * kWarps) {
+    a.spike[static_cast<int64_t>(c) * a.M + t] = -INFINITY;
+    if (t < a.tiles_t) a.flags[c * a.tiles_t + t] = 0;
+  }
+}
+
+enum { kScores = 0, kMax = 1, kGrad = 2 };
+
 struct LmParams {
-  int64_t M, D, V;
-  int Mp;               // rows of a buffer of P: M rounded up to whole tiles
-  int cols;             // vocabulary entries of a piece (the last may have fewer)
-  int c0, c1;           // the pieces of this launch
-  int w_row0;           // the first entry that the W maps hold
-  int make_scores;      // 0: P is there already, only the gradient is taken (one piece a launch)
-  int tiles_t, tiles_d; // token tiles; feature tiles
-  int d_steps;          // 128-deep steps of the hidden size
-  int slices;           // parts of the gradient's contraction
-  int band;             // token tiles of the gradient in bands of `band` (0: token tiles fastest)
-  int piece_parts;      // part_sum rows of a piece
+  int64_t M;            // tokens of this block
+  int64_t D;            // hidden size
+  int64_t cols;         // vocabulary entries of this piece
+  int64_t v0;           // the piece's first vocabulary entry
+  int red_steps;        // 128-deep steps of the whole contraction
+  int64_t red_len;      // contraction length (D, or cols)
+  int tiles_t, tiles_f; // token tiles; vocabulary tiles or feature tiles (256)
+  int slices;           // kGrad: parts of the contraction
+  int band;             // kGrad: token tiles in bands of `band` (0: token tiles fastest)
   int f16;
+  int redo;             // kScores: only the token tiles whose flag is set, with the raised R
+  int add;              // kGrad: add to the sums of the pieces before
   float range;
-  const int64_t* targets;   // clean: the target, or -1 for a token that does not count
-  float* refs;              // [pieces + 1][M] R, times log2(e); row 0 is the start
-  int* piece_ref;           // [pieces] the row of refs that holds R after a piece
-  float* spike;             // [pieces][M] largest logit beyond the range in a piece, or -inf
-  int* flags;               // [pieces][tiles_t] a row of the tile went beyond the range
-  int* any;                 // [pieces] one of them is set
-  unsigned* arrived;        // [pieces] the counter of a launch that starts with this piece
+  PrepArgs prep;            // kMax from the first piece on prepares the tokens itself
+  int prepare;
+  const float* ref;         // [M] R for this piece, times log2(e)
+  float* ref_next;          // [M] redo: R after this piece
+  float* spike;             // [M] largest logit beyond the range in this piece, or -inf
+  int* flags;               // [tiles_t] a row of the tile went beyond the range
   float* part_sum;          // [half vocabulary tile][M]
-  float* part_max;          // without a gradient: [half vocabulary tile][M], times log2(e)
-  float* acc;               // [slices][M][D]
+  float* part_max;          // kMax: [half vocabulary tile][M], times log2(e)
+  float* acc;               // kGrad: [slices][M][D]
   int* status;
   uint64_t wait_ns;
   int skip_stage0;
@@ -123,61 +216,24 @@ struct Ring {
   }
 };
 
-// One tile's work.
 struct Unit {
-  int t, f;             // token tile; vocabulary tile of the piece, or feature tile
-  int k0;               // first contraction element (of the hidden size, or of the piece)
+  int t, f;             // token tile; vocabulary or feature tile
+  int k0;               // first contraction element
   int nsub;             // 64-deep sub-blocks
   int slice;
 };
 
-// The units of one piece that a cluster takes, in order.  Scores after another piece's gradient:
-// the first `extra` clusters have one gradient unit more than the others, which is worth `skew`
-// units of scores, so the others go on for that many rounds alone.
-struct Piece {
-  int v0, cols, tiles_v;
-  int n_scores, n_grad, g_steps;
-  int full;             // rounds of scores that every cluster takes part in
-  int extra;
-  __device__ Piece(const LmParams& p, int c, int clusters, int first) {
-    v0 = c * p.cols;
-    cols = static_cast<int>(min(static_cast<int64_t>(p.cols), p.V - v0));
-    tiles_v = (cols + kTile - 1) / kTile;
-    n_scores = p.make_scores ? p.tiles_t * tiles_v : 0;
-    n_grad = p.tiles_t * p.tiles_d * p.slices;
-    g_steps = (cols + kStepK - 1) / kStepK;
-    extra = c > first && p.slices > 0 ? n_grad % clusters : 0;
-    const int skew = extra > 0 ? (p.cols / kStepK / p.slices + p.d_steps / 2) / p.d_steps : 0;
-    const int others = clusters - extra;
-    full = skew > 0 ? max(0, (n_scores - others * skew + clusters - 1) / clusters) : (n_scores + clusters - 1) / clusters;
-  }
-  // The cluster's score unit of round r, or -1.
-  __device__ __forceinline__ int score(int r, int cluster, int clusters) const {
-    int u;
-    if (r < full) u = r * clusters + cluster;
-    else if (cluster < extra) return -1;
-    else u = full * clusters + (r - full) * (clusters - extra) + cluster - extra;
-    return u < n_scores ? u : -1;
-  }
-};
-
-__device__ __forceinline__ Unit score_unit(const LmParams& p, int u) {
+template <int MODE>
+__device__ __forceinline__ Unit unit_of(const LmParams& p, int u) {
   Unit x;
-  x.t = u % p.tiles_t;
-  x.f = u / p.tiles_t;
-  x.k0 = 0;
-  x.nsub = static_cast<int>((p.D + kSub - 1) / kSub);
   x.slice = 0;
-  return x;
-}
-
-__device__ __forceinline__ Unit grad_unit(const LmParams& p, const Piece& pc, int u) {
-  Unit x;
-  const int tiles = p.tiles_t * p.tiles_d;
-  x.slice = u / tiles;
-  u -= x.slice * tiles;
-  if (p.band > 0) {
-    const int per = p.band * p.tiles_d;
+  if (MODE == kGrad) {
+    const int tiles = p.tiles_t * p.tiles_f;
+    x.slice = u / tiles;
+    u -= x.slice * tiles;
+  }
+  if (MODE == kGrad && p.band > 0) {
+    const int per = p.band * p.tiles_f;
     const int bi = u / per, t0 = bi * p.band;
     const int bt = min(p.band, p.tiles_t - t0);
     const int idx = u - bi * per;
@@ -187,11 +243,14 @@ __device__ __forceinline__ Unit grad_unit(const LmParams& p, const Piece& pc, in
     x.t = u % p.tiles_t;
     x.f = u / p.tiles_t;
   }
-  // slices differ by a step at most; none is empty (slices <= g_steps)
-  const int s0 = static_cast<int>(static_cast<int64_t>(pc.g_steps) * x.slice / p.slices);
-  const int s1 = static_cast<int>(static_cast<int64_t>(pc.g_steps) * (x.slice + 1) / p.slices);
+  int s0 = 0, s1 = p.red_steps;
+  if (MODE == kGrad) {   // slices differ by a step at most; none is empty (slices <= red_steps)
+    s0 = static_cast<int>(static_cast<int64_t>(p.red_steps) * x.slice / p.slices);
+    s1 = static_cast<int>(static_cast<int64_t>(p.red_steps) * (x.slice + 1) / p.slices);
+  }
   x.k0 = s0 * kStepK;
-  x.nsub = (min(pc.cols, s1 * kStepK) - x.k0 + kSub - 1) / kSub;
+  const int len = min(static_cast<int>(p.red_len), s1 * kStepK) - x.k0;
+  x.nsub = (len + kSub - 1) / kSub;
   return x;
 }
 
@@ -226,19 +285,12 @@ __device__ __forceinline__ void atomic_max_float(float* a, float v) {
   else atomicMin(reinterpret_cast<unsigned*>(a), __float_as_uint(v));
 }
 
-__device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
-  unsigned v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-
-// Maps: x and W for the scores (K-major boxes of 128 rows), W for the gradient (64 features x 64
-// entries, MN-major), P as it is stored (boxes of 32 x 32) and read (128 rows).
-template <bool kGradient>
+// tm_a / tm_b: kScores, kMax: x and W[piece] (K-major); kGrad: W[piece] (MN-major) and P.
+// tm_p: P as the kScores epilogue stores it.
+template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
-lm_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-        const __grid_constant__ CUtensorMap tm_wg, const __grid_constant__ CUtensorMap tm_p,
-        const __grid_constant__ CUtensorMap tm_pg, const LmParams p) {
+lm_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+        const __grid_constant__ CUtensorMap tm_p, const LmParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -247,17 +299,32 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtens
   uint64_t* bars = reinterpret_cast<uint64_t*>(base_ptr + kStages * kStageBytes + kEpiWarps * kBoxes * kBoxBytes);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kNumBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars) + 1;
-  volatile int* raise = reinterpret_cast<volatile int*>(bars + kNumBars) + 2;   // the piece has flags
   auto bar = [&](int i) { return smem_u32(bars + i); };
   auto stage_a = [&](int s) { return base + s * kStageBytes; };
   auto stage_b = [&](int s) { return base + s * kStageBytes + kSubs * kSubBytes; };
   const uint32_t rank = cluster_ctarank();
   auto lead_bar = [&](int i) { return mapa_shared(bar(i), 0); };
-  const int cluster = blockIdx.x / kCluster;
-  const int clusters = gridDim.x / kCluster;
+  const int cluster_id = blockIdx.x / kCluster;
+  const int n_clusters = gridDim.x / kCluster;
+  const int total = p.tiles_t * p.tiles_f * (MODE == kGrad ? p.slices : 1);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  if (MODE == kScores && p.redo) {
+    // a repeated pass raises R; without a flag it does nothing else
+    pdl_allow_next();
+    pdl_wait();
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; t < p.M;
+         t += static_cast<int64_t>(gridDim.x) * kThreads)
+      p.ref_next[t] = fmaxf(p.ref[t], p.spike[t]);
+    bool any = false;
+    for (int i = lane; i < p.tiles_t; i += 32) any |= p.flags[i] != 0;
+    if (!__any_sync(0xffffffffu, any)) return;
+  }
+  if (threadIdx.x == 32) {   // the maps are fetched while the barriers are set up
+    for (const CUtensorMap* m : {&tm_a, &tm_b, &tm_p})
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(kBarFull + s), 1);
@@ -268,10 +335,7 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtens
       mbar_init(bar(kBarAccEmpty + b), kEpiWarps * kCluster);
     }
     mbar_init(bar(kBarDone), 1);
-    mbar_init(bar(kBarPhase), 1);
-    mbar_init(bar(kBarAck), 1);
     *abort_flag = 0;
-    *raise = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_allow_next();
@@ -287,157 +351,110 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtens
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, p.status, p.wait_ns); };
 
-  // Every role walks the same units: each piece's scores, the phase that ends them, the flagged
-  // tiles' scores again and their phase, the gradient.  `scores`, `phase` and `grad` return false
-  // when a wait gave up.
-  unsigned phases = 0;
-  bool raised = false;      // the piece has flags (each role's copy, taken at its phase)
-  auto walk = [&](auto&& scores, auto&& phase, auto&& grad) {
-    for (int c = p.c0; c < p.c1; ++c) {
-      const Piece pc(p, c, clusters, p.c0);
-      for (int r = 0;; ++r) {
-        const int u = pc.score(r, cluster, clusters);
-        if (u < 0) break;
-        if (!scores(pc, c, score_unit(p, u), false)) return;
-      }
-      if (!kGradient) continue;
-      if (p.make_scores) {
-        if (!phase(c, false)) return;
-        if (raised) {
-          for (int u = cluster; u < pc.n_scores; u += clusters) {
-            const Unit un = score_unit(p, u);
-            if (__ldcg(p.flags + c * p.tiles_t + un.t) != 0 && !scores(pc, c, un, true)) return;
-          }
-          if (!phase(c, true)) return;
-        }
-      }
-      for (int u = cluster; u < pc.n_grad; u += clusters)
-        if (!grad(pc, c, grad_unit(p, pc, u))) return;
-    }
-  };
+  // every role walks the same units; a repeated pass leaves out the token tiles without a flag
+  auto runs = [&](const Unit& un) { return !(MODE == kScores && p.redo) || p.flags[un.t] != 0; };
 
   if (warp == 0) {
     if (lane == 0) {
-      // ---------------- TMA producer, and the CTA's look-out for phases ----------------
-      Ring r;
+      // ---------------- TMA producer ----------------
+      bool ok = true;
+      Ring c;
       int64_t issued = 0;
       int64_t lt = 0;
-      bool ok = true;
-      auto load = [&](const Unit& un, auto&& copy) {
+      for (int u = cluster_id; ok && u < total; u += n_clusters) {
+        const Unit un = unit_of<MODE>(p, u);
+        if (!runs(un)) continue;
+        // A rows / B rows of this CTA, as tensor coordinates
+        const int t_row = static_cast<int>(un.t * kTile) + static_cast<int>(rank) * kHalf;
+        const int f_row = static_cast<int>(un.f * kTile) + static_cast<int>(rank) * kHalf;
         const int nsteps = (un.nsub + kSubs - 1) / kSubs;
-        for (int st = 0; st < nsteps; ++st, r.advance()) {
-          if (!wait(kBarEmpty + r.s, r.ph ^ 1u)) return ok = false;
-          if (p.skip_stage0 && blockIdx.x == 0 && issued == 0) {   // the stage's waits will run out
+        for (int st = 0; st < nsteps; ++st, c.advance()) {
+          const int s = c.s;
+          if (!mbar_wait(bar(kBarEmpty + s), c.ph ^ 1u, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
+          const uint32_t full = lead_bar(kBarFull + s);
+          if (p.skip_stage0 && blockIdx.x == 0 && issued == 0) {
             ++issued;
             continue;
           }
           // odd units walk the contraction backwards, so a round starts on what the last one
           // left in L2
           const int kst = (lt & 1) ? nsteps - 1 - st : st;
+          const int k0 = static_cast<int>(un.k0) + kst * kStepK;
           const int subs = min(kSubs, un.nsub - kst * kSubs);
-          if (rank == 0) mbar_expect_tx(bar(kBarFull + r.s), kCluster * 2 * subs * kSubBytes);
-          for (int q = 0; q < subs; ++q)
-            copy(stage_a(r.s) + q * kSubBytes, stage_b(r.s) + q * kSubBytes, lead_bar(kBarFull + r.s),
-                 un.k0 + (kst * kSubs + q) * kSub);
+          if (rank == 0) mbar_expect_tx(bar(kBarFull + s), kCluster * 2 * subs * kSubBytes);
+          for (int q = 0; q < subs; ++q) {
+            const uint32_t a = stage_a(s) + q * kSubBytes;
+            const uint32_t b = stage_b(s) + q * kSubBytes;
+            if (MODE == kGrad) {
+              tma_load_2d_pair(a, &tm_a, full, f_row, k0 + q * kSub);
+              tma_load_2d_pair(a + kHalfSub, &tm_a, full, f_row + 64, k0 + q * kSub);
+              tma_load_2d_pair(b, &tm_b, full, k0 + q * kSub, t_row);
+            } else {
+              tma_load_2d_pair(a, &tm_a, full, k0 + q * kSub, t_row);
+              tma_load_2d_pair(b, &tm_b, full, k0 + q * kSub, f_row);
+            }
+          }
           ++issued;
         }
         ++lt;
-        return true;
-      };
-      const int half = static_cast<int>(rank) * kHalf;
-      walk(
-          [&](const Piece& pc, int, const Unit& un, bool) {
-            const int t = un.t * kTile + half, v = pc.v0 - p.w_row0 + un.f * kTile + half;
-            return load(un, [&](uint32_t a, uint32_t b, uint32_t full, int k) {
-              tma_load_2d_pair(a, &tm_x, full, k, t);
-              tma_load_2d_pair(b, &tm_w, full, k, v);
-            });
-          },
-          [&](int c, bool again) {
-            // every epilogue warp of the launch has arrived: P is written, and who went beyond the
-            // range is known
-            ++phases;
-            const unsigned target = phases * kEpiWarps * gridDim.x;
-            const uint64_t t0 = global_ns();
-            for (uint32_t i = 1; ld_acquire(p.arrived + p.c0) < target; ++i) {
-              __nanosleep(64);
-              if ((i & 15u) == 0 && (*abort_flag || global_ns() - t0 > p.wait_ns)) {
-                *abort_flag = 1;
-                atomicCAS(p.status, 0, static_cast<int>(NF4_ERR_TIMEOUT));
-                return ok = false;
-              }
-            }
-            asm volatile("fence.proxy.async;" ::: "memory");   // P's stores before this CTA's TMA loads
-            // the issuer has taken the phase before (the epilogue's arrival says so itself)
-            if (rank == 0 && phases > 1 && !wait(kBarAck, (phases - 2) & 1u)) return ok = false;
-            raised = !again && __ldcg(p.any + c) != 0;
-            *raise = raised;
-            mbar_arrive(bar(kBarPhase));
-            return true;
-          },
-          [&](const Piece& pc, int c, const Unit& un) {
-            const int t = (c & 1) * p.Mp + un.t * kTile + half, f = un.f * kTile + half, v = pc.v0 - p.w_row0;
-            return load(un, [&](uint32_t a, uint32_t b, uint32_t full, int k) {
-              tma_load_2d_pair(a, &tm_wg, full, f, v + k);
-              tma_load_2d_pair(a + kHalfSub, &tm_wg, full, f + 64, v + k);
-              tma_load_2d_pair(b, &tm_pg, full, k, t);
-            });
-          });
+      }
       if (ok) {
         for (int k = 0; k < kStages; ++k) {
-          if (!wait(kBarEmpty + r.s, r.ph ^ 1u)) break;
-          r.advance();
+          if (!mbar_wait(bar(kBarEmpty + c.s), c.ph ^ 1u, abort_flag, p.status, p.wait_ns)) break;
+          c.advance();
         }
-      } else if (rank == 0) {   // let copies in flight land before the CTA exits
+      } else if (rank == 0) {
+        int ds = c.s;
+        uint32_t dph = c.ph;
         for (int64_t k = 0; k < kStages && k < issued; ++k) {
-          if (r.s == 0) r.s = kStages - 1, r.ph ^= 1u;
-          else --r.s;
-          mbar_drain(bar(kBarFull + r.s), r.ph);
+          if (ds == 0) ds = kStages - 1, dph ^= 1u;
+          else --ds;
+          mbar_drain(bar(kBarFull + ds), dph);
         }
       }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       // ---------------- MMA issuer (even CTA) ----------------
-      Ring r;
+      const uint32_t idesc = idesc_16(kTile, kTile, MODE == kGrad ? 1u : 0u, p.f16 ? 1u : 0u);
+      bool ok = true;
+      Ring c;
       int64_t lt = 0;
-      auto issue = [&](const Unit& un, bool mn_major) {
-        const uint32_t idesc = idesc_16(kTile, kTile, mn_major ? 1u : 0u, p.f16 ? 1u : 0u);
+      for (int u = cluster_id; ok && u < total; u += n_clusters) {
+        const Unit un = unit_of<MODE>(p, u);
+        if (!runs(un)) continue;
         const int nsteps = (un.nsub + kSubs - 1) / kSubs;
         const uint32_t b = static_cast<uint32_t>(lt) & 1u;
-        if (!wait(kBarAccEmpty + b, (static_cast<uint32_t>(lt >> 1) & 1u) ^ 1u)) return false;
+        if (!mbar_wait(bar(kBarAccEmpty + b), (static_cast<uint32_t>(lt >> 1) & 1u) ^ 1u, abort_flag, p.status,
+                       p.wait_ns)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + b * kTile;
-        for (int st = 0; st < nsteps; ++st, r.advance()) {
-          if (!wait(kBarFull + r.s, r.ph)) return false;
+        for (int st = 0; st < nsteps; ++st, c.advance()) {
+          if (!mbar_wait(bar(kBarFull + c.s), c.ph, abort_flag, p.status, p.wait_ns)) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
           const int kst = (lt & 1) ? nsteps - 1 - st : st;
           const int subs = min(kSubs, un.nsub - kst * kSubs);
           for (int q = 0; q < subs; ++q)
 #pragma unroll
             for (int kk = 0; kk < kSub / 16; ++kk) {
-              const uint32_t sa = stage_a(r.s) + q * kSubBytes;
-              const uint64_t adesc =
-                  mn_major ? smem_desc(sa + kk * 2048, kHalfSub, 1024) : smem_desc(sa + kk * 32, 16, 1024);
-              const uint64_t bdesc = smem_desc(stage_b(r.s) + q * kSubBytes + kk * 32, 16, 1024);
+              const uint32_t sa = stage_a(c.s) + q * kSubBytes;
+              const uint64_t adesc = MODE == kGrad ? smem_desc(sa + kk * 2048, kHalfSub, 1024)
+                                                   : smem_desc(sa + kk * 32, 16, 1024);
+              const uint64_t bdesc = smem_desc(stage_b(c.s) + q * kSubBytes + kk * 32, 16, 1024);
               umma_bf16_pair(d_tmem, adesc, bdesc, idesc, (st > 0 || q > 0 || kk > 0) ? 1u : 0u);
             }
-          umma_commit_pair_mc(bar(kBarEmpty + r.s), 0x3);
+          umma_commit_pair_mc(bar(kBarEmpty + c.s), 0x3);
           if (st == nsteps - 1) umma_commit_pair_mc(bar(kBarAccFull + b), 0x3);
         }
         ++lt;
-        return true;
-      };
-      walk([&](const Piece&, int, const Unit& un, bool) { return issue(un, false); },
-           [&](int, bool) {
-             if (!wait(kBarPhase, (phases++) & 1u)) return false;
-             raised = *raise != 0;
-             mbar_arrive(bar(kBarAck));
-             return true;
-           },
-           [&](const Piece&, int, const Unit& un) { return issue(un, true); });
+      }
       umma_commit_pair_mc(bar(kBarDone), 0x1);
       mbar_drain(bar(kBarDone), 0);
     }
@@ -449,181 +466,146 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtens
     const uint32_t my_box = boxes + static_cast<uint32_t>((warp - 2) * kBoxes * kBoxBytes);
     uint32_t nst = 0;
     int64_t lt = 0;
-    int ref_row = p.c0 == 0 || !kGradient ? 0 : __ldcg(p.piece_ref + p.c0 - 1);   // R of the piece at hand
-    int old_row = ref_row;                                                       // R of the sums so far
-    // the accumulator of the next unit, ready
-    auto ready = [&](uint32_t* taddr) {
+    if (MODE == kMax && p.prepare) {   // the tokens, under the first tiles' products; only lm_finish reads them
+      for (int64_t t = static_cast<int64_t>(blockIdx.x) * kEpiWarps + warp - 2; t < p.M;
+           t += static_cast<int64_t>(gridDim.x) * kEpiWarps)
+        prep_token<false, 1>(p.prep, t, lane, nullptr, p.status);
+    }
+    for (int u = cluster_id; u < total; u += n_clusters) {
+      const Unit un = unit_of<MODE>(p, u);
+      if (!runs(un)) continue;
       const uint32_t b = static_cast<uint32_t>(lt) & 1u;
-      if (!__all_sync(0xffffffffu, wait(kBarAccFull + b, static_cast<uint32_t>(lt >> 1) & 1u))) return false;
+      const uint32_t aph = static_cast<uint32_t>(lt >> 1) & 1u;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarAccFull + b), aph, abort_flag, p.status, p.wait_ns))) break;
       tc_fence_after();
-      *taddr = tmem_base + b * kTile + (static_cast<uint32_t>(quarter * 32) << 16);
-      return true;
-    };
-    auto release = [&]() {
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(lead_bar(kBarAccEmpty + (static_cast<uint32_t>(lt) & 1u)));
-      ++lt;
-    };
-    walk(
-        [&](const Piece& pc, int c, const Unit& un, bool again) {
-          // lane: one token; columns: vocabulary entries
-          uint32_t taddr;
-          if (!ready(&taddr)) return false;
-          const int t0w = un.t * kTile + static_cast<int>(rank) * kHalf + quarter * 32, t = t0w + lane;
-          const int64_t y = t < p.M ? p.targets[t] : -1;
-          const bool live = y >= 0;
-          const int64_t yc64 = y - pc.v0 - un.f * kTile;
-          const int yc = (live && yc64 >= cb && yc64 < ce) ? static_cast<int>(yc64) : -1;
-          const int valid = min(kTile, pc.cols - un.f * kTile);
-          const bool masked = __any_sync(0xffffffffu, yc >= 0) || valid < ce;
-          const int64_t part = (static_cast<int64_t>(c) * p.piece_parts + un.f * 2 + half) * p.M + t;
-          const float* ref = p.refs + static_cast<int64_t>(ref_row) * p.M;
-          float* spike = p.spike + static_cast<int64_t>(c) * p.M;
-          float r2 = 0.0f;
-          if (kGradient && t < p.M) {
-            r2 = __ldcg(ref + t);
-            if (again) r2 = fmaxf(r2, __ldcg(spike + t));
-          }
-          const uint32_t keep = live ? 0xffffffffu : 0u;
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          // columns at a time in registers: all of them where their maximum comes first; the last
-          // load frees the accumulator for the unit after next
-          constexpr int kAt = kGradient ? 2 : kEpiCols / 32;
-#pragma unroll
-          for (int h0 = 0; h0 < kEpiCols / 32; h0 += kAt) {
-            uint32_t v[kAt][32];
-            const int cp = cb + 32 * h0;
-#pragma unroll
-            for (int h = 0; h < kAt; ++h) tmem_ld32(taddr + cp + 32 * h, v[h]);
-            tmem_ld_wait();
-            if (h0 + kAt == kEpiCols / 32) release();
-            if (masked) {
-#pragma unroll
-              for (int h = 0; h < kAt; ++h)
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (cp + 32 * h + j == yc || cp + 32 * h + j >= valid) v[h][j] = 0xff800000u;   // -inf
-            }
-#pragma unroll
-            for (int h = 0; h < kAt; ++h)
-#pragma unroll
-              for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(v[h][j]));
-            if (!kGradient) {
-              const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-              const float m2 = mx == -INFINITY ? 0.0f : mx * kLog2e;
-#pragma unroll
-              for (int h = 0; h < kAt; ++h)
-#pragma unroll
-                for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(__uint_as_float(v[h][j]), kLog2e, -m2));
-              if (t < p.M) {
-                p.part_max[part] = mx == -INFINITY ? mx : m2;
-                p.part_sum[part] = (s[0] + s[1]) + (s[2] + s[3]);
-              }
-              return true;
-            }
-#pragma unroll
-            for (int h = 0; h < kAt; ++h, ++nst) {
-              const uint32_t box = my_box + (nst & 1u) * kBoxBytes;
-              uint32_t o[16];
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const float e0 = ex2(fmaf(__uint_as_float(v[h][2 * k]), kLog2e, -r2));
-                const float e1 = ex2(fmaf(__uint_as_float(v[h][2 * k + 1]), kLog2e, -r2));
-                s[k & 3] += e0;
-                s[k & 3] += e1;
-                o[k] = pack2(e0, e1, p.f16) & keep;
-              }
-              if (lane == 0) bulk_wait_read<1>();      // the store that last used this box has read it
-              __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                // row `lane` of the box, 16-byte column k, 64-byte swizzle
-                const uint32_t col = static_cast<uint32_t>(k) ^ ((static_cast<uint32_t>(lane) >> 1) & 3u);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * (kBoxCols * 2) + col * 16),
-                             "r"(o[4 * k]), "r"(o[4 * k + 1]), "r"(o[4 * k + 2]), "r"(o[4 * k + 3])
-                             : "memory");
-              }
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              __syncwarp();
-              if (lane == 0) {   // (rows past M fill the buffer's last tile with zeros)
-                tma_store_2d(&tm_p, box, un.f * kTile + cp + h * kBoxCols, (c & 1) * p.Mp + t0w);
-                bulk_commit();
-              }
-            }
-          }
-          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          if (t < p.M) {
-            p.part_sum[part] = live ? (s[0] + s[1]) + (s[2] + s[3]) : 0.0f;
-            const float m2 = mx * kLog2e;
-            if (live && !again && m2 > r2 + p.range) {
-              atomic_max_float(spike + t, m2);
-              p.flags[c * p.tiles_t + un.t] = 1;
-              p.any[c] = 1;
-            }
-          }
-          return true;
-        },
-        [&](int c, bool again) {
-          if (!again) old_row = ref_row;
-          if (again) {   // the raised R, for the pieces after this one
-            if (blockIdx.x == 0)
-              for (int64_t t = threadIdx.x - 64; t < p.M; t += 32 * kEpiWarps)
-                p.refs[(c + 1) * p.M + t] = fmaxf(__ldcg(p.refs + ref_row * p.M + t), __ldcg(p.spike + c * p.M + t));
-            ref_row = c + 1;
-          }
-          if (lane == 0) bulk_wait_all();     // this warp's stores of P are complete
-          __syncwarp();
-          __threadfence();
-          if (lane == 0) atomicAdd(p.arrived + p.c0, 1u);
-          const bool got = wait(kBarPhase, (phases++) & 1u);
-          if (!__all_sync(0xffffffffu, got)) return false;
-          raised = *raise != 0;
-          if (blockIdx.x == 0 && threadIdx.x == 64) p.piece_ref[c] = ref_row;
-          return true;
-        },
-        [&](const Piece&, int c, const Unit& un) {
-          // lane: one feature; columns: tokens.  The sums so far are in units of 2^-refs[old_row],
-          // this piece's in 2^-refs[row]
-          uint32_t taddr;
-          if (!ready(&taddr)) return false;
-          const int row = p.make_scores ? ref_row : c + 1;
-          const int before = p.make_scores ? old_row : c;
-          const float* r0 = p.refs + static_cast<int64_t>(before) * p.M;
-          const float* r1 = p.refs + static_cast<int64_t>(row) * p.M;
-          const int64_t f = static_cast<int64_t>(un.f) * kTile + static_cast<int64_t>(rank) * kHalf + lrow;
-          float* dst = p.acc + static_cast<int64_t>(un.slice) * p.M * p.D + f;
-          const int64_t t0 = static_cast<int64_t>(un.t) * kTile;
+      const uint32_t taddr = tmem_base + b * kTile + (static_cast<uint32_t>(quarter * 32) << 16);
+      if (MODE == kGrad) {
+        // lane: one feature; columns: tokens.  Sums of the pieces before are in units of
+        // 2^-ref; this piece's in 2^-ref_next
+        const int64_t f = static_cast<int64_t>(un.f) * kTile + static_cast<int64_t>(rank) * kHalf + lrow;
+        float* dst = p.acc + static_cast<int64_t>(un.slice) * p.M * p.D + f;
+        const int64_t t0 = static_cast<int64_t>(un.t) * kTile;
 #pragma unroll 1
-          for (int c0 = cb; c0 < ce && t0 + c0 < p.M; c0 += 16) {
-            uint32_t v[16];
-            tmem_ld16(taddr + c0, v);
-            float old[16];
-            if (c > 0) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int64_t t = t0 + c0 + j;
-                old[j] = (t < p.M && f < p.D) ? dst[t * p.D] : 0.0f;
-                if (row != before && t < p.M) {
-                  const float a = __ldcg(r0 + t), b = __ldcg(r1 + t);
-                  if (a != b) old[j] *= exp2f(a - b);
-                }
-              }
-            }
-            tmem_ld_wait();
+        for (int c0 = cb; c0 < ce && t0 + c0 < p.M; c0 += 16) {
+          uint32_t v[16];
+          tmem_ld16(taddr + c0, v);
+          float old[16];
+          if (p.add) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const int64_t t = t0 + c0 + j;
-              float s = __uint_as_float(v[j]);
-              if (c > 0) s += old[j];
-              if (t < p.M && f < p.D) dst[t * p.D] = s;
+              old[j] = (t < p.M && f < p.D) ? dst[t * p.D] : 0.0f;
+              const float r0 = t < p.M ? p.ref[t] : 0.0f, r1 = t < p.M ? p.ref_next[t] : 0.0f;
+              if (r0 != r1) old[j] *= exp2f(r0 - r1);
             }
           }
-          release();
-          return true;
-        });
-    if (kGradient && lane == 0) bulk_wait_all();
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int64_t t = t0 + c0 + j;
+            float s = __uint_as_float(v[j]);
+            if (p.add) s += old[j];
+            if (t < p.M && f < p.D) dst[t * p.D] = s;
+          }
+        }
+      } else {
+        // lane: one token; columns: vocabulary entries
+        const int64_t t0w = static_cast<int64_t>(un.t) * kTile + static_cast<int64_t>(rank) * kHalf + quarter * 32;
+        const int64_t t = t0w + lane;
+        const int64_t c_tile = static_cast<int64_t>(un.f) * kTile;   // first column within the piece
+        const int64_t y = t < p.M ? clean_target(p.prep.targets[t], p.prep.V, p.prep.ignore) : -1;
+        const bool live = y >= 0;
+        const int64_t yc64 = y - p.v0 - c_tile;
+        const int yc = (live && yc64 >= cb && yc64 < ce) ? static_cast<int>(yc64) : -1;
+        const int valid = static_cast<int>(min(static_cast<int64_t>(kTile), p.cols - c_tile));
+        const bool masked = __any_sync(0xffffffffu, yc >= 0) || valid < ce;
+        const int64_t part = (static_cast<int64_t>(un.f) * 2 + half) * p.M + t;
+        // the warp's whole part to registers, which frees the accumulator for the unit after next
+        uint32_t v[kEpiCols / 32][32];
+#pragma unroll
+        for (int h = 0; h < kEpiCols / 32; ++h) tmem_ld32(taddr + cb + 32 * h, v[h]);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(lead_bar(kBarAccEmpty + b));
+        if (masked) {
+#pragma unroll
+          for (int h = 0; h < kEpiCols / 32; ++h)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (cb + 32 * h + j == yc || cb + 32 * h + j >= valid) v[h][j] = 0xff800000u;   // -inf
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int h = 0; h < kEpiCols / 32; ++h)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(v[h][j]));
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (MODE == kMax) {
+          const float m2 = mx == -INFINITY ? 0.0f : mx * kLog2e;
+#pragma unroll
+          for (int h = 0; h < kEpiCols / 32; ++h)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(__uint_as_float(v[h][j]), kLog2e, -m2));
+          if (t < p.M) {
+            p.part_max[part] = mx == -INFINITY ? mx : m2;
+            p.part_sum[part] = (s[0] + s[1]) + (s[2] + s[3]);
+          }
+        } else {
+          float r2 = t < p.M ? p.ref[t] : 0.0f;
+          if (p.redo && t < p.M) r2 = fmaxf(r2, p.spike[t]);
+          const uint32_t keep = live ? 0xffffffffu : 0u;
+#pragma unroll
+          for (int h = 0; h < kEpiCols / kBoxCols; ++h, ++nst) {
+            const uint32_t box = my_box + (nst & 1u) * kBoxBytes;
+            uint32_t o[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float e0 = ex2(fmaf(__uint_as_float(v[h][2 * k]), kLog2e, -r2));
+              const float e1 = ex2(fmaf(__uint_as_float(v[h][2 * k + 1]), kLog2e, -r2));
+              s[k & 3] += e0;
+              s[k & 3] += e1;
+              o[k] = pack2(e0, e1, p.f16) & keep;
+            }
+            if (lane == 0) bulk_wait_read<1>();      // the store that last used this box has read it
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              // row `lane` of the box, 16-byte column k, 64-byte swizzle
+              const uint32_t col = static_cast<uint32_t>(k) ^ ((static_cast<uint32_t>(lane) >> 1) & 3u);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * (kBoxCols * 2) + col * 16),
+                           "r"(o[4 * k]), "r"(o[4 * k + 1]), "r"(o[4 * k + 2]), "r"(o[4 * k + 3])
+                           : "memory");
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              const int c0 = cb + h * kBoxCols;
+              // the contraction over P goes on in zeros up to the next 64 columns
+              if (t0w < p.M && c0 < (valid + kSub - 1) / kSub * kSub)
+                tma_store_2d(&tm_p, box, static_cast<int>(c_tile) + c0, static_cast<int>(t0w));
+              bulk_commit();
+            }
+          }
+          if (t < p.M) {
+            p.part_sum[part] = live ? (s[0] + s[1]) + (s[2] + s[3]) : 0.0f;
+            const float m2 = mx * kLog2e;
+            if (live && !p.redo && m2 > r2 + p.range) {
+              atomic_max_float(p.spike + t, m2);
+              p.flags[un.t] = 1;
+            }
+          }
+        }
+      }
+      if (MODE == kGrad) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(lead_bar(kBarAccEmpty + b));
+      }
+      ++lt;
+    }
+    if (MODE == kScores && lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -634,26 +616,6 @@ lm_gemm(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtens
                  : "memory");
   }
 }
-
-__device__ __forceinline__ float lo16(uint32_t w, int f16) {
-  return f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(w & 0xffffu))) : __uint_as_float(w << 16);
-}
-__device__ __forceinline__ float hi16(uint32_t w, int f16) {
-  return f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16))) : __uint_as_float(w & 0xffff0000u);
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// The target of a token, or -1 where it does not count.
-__device__ __forceinline__ int64_t clean_target(int64_t y, int64_t V, int64_t ignore) {
-  return y >= 0 && y < V && y != ignore ? y : -1;
-}
-// Entry i of the kSamples of a vocabulary.
-__device__ __forceinline__ int64_t sample_of(int i, int64_t V) { return V * i / kSamples; }
 
 // Rows of a stored head: out[t][d..d+7] = T16(nf4[code] * a'), the bits nf4_dequantize writes, of
 // the targets' rows (0 for a token that does not count) and then of the samples'.
@@ -684,83 +646,21 @@ __global__ void lm_stored_rows(const Nf4View W, const DecodeTables tabs, const i
   }
 }
 
-__device__ __forceinline__ float dot8(uint4 u, uint4 v, int f16, float s) {
-  const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    s = fmaf(lo16(uu[k], f16), lo16(vv[k], f16), s);
-    s = fmaf(hi16(uu[k], f16), hi16(vv[k], f16), s);
-  }
-  return s;
-}
-
-constexpr int kPrepThreads = 128;
-
-// One CTA per token: clean[t]; zt[t] = x[t] . W[y] in fp32; R's start (ref, times log2(e), where a
-// gradient is asked for: kSample takes the samples' logits too); the pieces' spikes and flags.
-// A target outside [0, V) that is not ignore_index sets NF4_ERR_ARG.
-// rows: W, or with by_token the decoded rows of the targets and then of the samples.
+// One CTA per token, where the pass that follows needs them ready.
+constexpr int kPrepWarps = 4;
 template <bool kSample>
-__global__ void __launch_bounds__(kPrepThreads)
-lm_prep(const uint4* x, const uint4* rows, int by_token, const int64_t* targets, int64_t M, int64_t V, int64_t ignore,
-        int64_t D8, int f16, int64_t* clean, float* zt, float* ref, float* spike, int* flags, int* any,
-        unsigned* arrived, int* piece_ref, int pieces, int tiles_t, int* status) {
-  constexpr int kDots = kSample ? 1 + kSamples : 1;
-  __shared__ float red[kPrepThreads / 32][kDots];
+__global__ void __launch_bounds__(kPrepWarps * 32) lm_prep(const PrepArgs a, int* status) {
+  __shared__ float red[kPrepWarps][1 + kSamples];
   pdl_allow_next();
   pdl_wait();
-  const int64_t t = blockIdx.x;
-  const int64_t given = targets[t], y = clean_target(given, V, ignore);
-  float s[kDots];
-#pragma unroll
-  for (int k = 0; k < kDots; ++k) s[k] = 0.0f;
-  if (y >= 0) {
-    const uint4* a = x + t * D8;
-    const uint4* w = rows + (by_token ? t : y) * D8;
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < D8; i += kPrepThreads) {
-      const uint4 u = a[i];
-      s[0] = dot8(u, w[i], f16, s[0]);
-      if (kSample) {
-#pragma unroll
-        for (int k = 0; k < kDots - 1; ++k)
-          s[1 + k] = dot8(u, rows[(by_token ? M + k : sample_of(k, V)) * D8 + i], f16, s[1 + k]);
-      }
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kDots; ++k) {
-    s[k] = warp_sum(s[k]);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5][k] = s[k];
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float z = 0.0f, top = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kDots; ++k) {
-      float v = 0.0f;
-      for (int q = 0; q < kPrepThreads / 32; ++q) v += red[q][k];
-      if (k == 0) z = v;
-      top = fmaxf(top, v);
-    }
-    clean[t] = y;
-    zt[t] = z;
-    if (ref != nullptr) ref[t] = (kSample ? top : z) * kLog2e;
-    if (y < 0 && given != ignore) atomicCAS(status, 0, static_cast<int>(NF4_ERR_ARG));
-  }
-  for (int c = threadIdx.x; c < pieces; c += kPrepThreads) {
-    spike[static_cast<int64_t>(c) * M + t] = -INFINITY;
-    if (t < tiles_t) flags[c * tiles_t + t] = 0;
-    if (t == 0) any[c] = 0, arrived[c] = 0, piece_ref[c] = c + 1;
-  }
+  prep_token<kSample, kPrepWarps>(a, blockIdx.x, threadIdx.x, red, status);
 }
 
 struct FinishArgs {
   int64_t M, D8;
   const float* part_sum;    // [parts][M]
   const float* part_max;    // given: each part's sum is relative to it; else to its piece's R
-  const float* refs;        // [pieces + 1][M]: R after a piece is row piece_ref[piece], the last what dx's sums are relative to
-  const int* piece_ref;
+  const float* refs;        // [pieces + 1][M]: a piece's R is row piece + 1, the last is what dx's sums are relative to
   int parts, piece_parts, pieces;
   const float* zt;
   const int64_t* clean;
@@ -788,21 +688,12 @@ __global__ void __launch_bounds__(kFinThreads) lm_finish(const FinishArgs f) {
   const int k = threadIdx.x % kFinTokens, i0 = threadIdx.x / kFinTokens, warp = threadIdx.x >> 5;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kFinTokens, t = t0 + k;
   const bool in = t < f.M;
-  const float z = in ? f.zt[t] : 0.0f;
-  float ref = in && f.part_max == nullptr ? f.refs[static_cast<int64_t>(f.piece_ref[f.pieces - 1]) * f.M + t] : z * kLog2e;
-  if (f.part_max != nullptr) {
-    if (in)
-      for (int i = i0; i < f.parts; i += kFinThreads / kFinTokens)
-        ref = fmaxf(ref, f.part_max[static_cast<int64_t>(i) * f.M + t]);
-#pragma unroll
-    for (int o = 16; o >= kFinTokens; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
-    if ((threadIdx.x & 31) < kFinTokens) red[warp][k] = ref;
-    __syncthreads();
-    for (int q = 0; q < kFinThreads / 32; ++q) ref = fmaxf(ref, red[q][k]);
-    __syncthreads();
-  }
-  // dx's items of this CTA (8 features of one token each); a thread's first one is gathered while
-  // the totals' loads are under way
+  const int64_t tc = min(t, f.M - 1);       // (a token past the end repeats the last)
+  const int64_t yt = f.clean[tc];
+  const float z = f.zt[tc];
+  const float g0 = f.gscale == nullptr ? 1.0f : f.gscale[f.gscale_per_row ? tc : 0];
+  constexpr int kStep = kFinThreads / kFinTokens, kAt = 8;     // parts a round: kAt loads of each of kStep threads
+  // dx's items of this CTA (8 features of one token each)
   const int64_t n = f.M * f.D8;
   const int64_t d0 = f.D8 * blockIdx.y / gridDim.y;
   const int dn = f.acc == nullptr ? 0 : static_cast<int>(f.D8 * (blockIdx.y + 1) / gridDim.y - d0);
@@ -812,32 +703,61 @@ __global__ void __launch_bounds__(kFinThreads) lm_finish(const FinishArgs f) {
   auto gather = [&](int j) {
     const int tk = j / dn;
     const int64_t d = d0 + j - tk * dn, at = (t0 + tk) * f.D8 + d, y = f.clean[t0 + tk];
-    w = f.rows[(f.by_token ? t0 + tk : max(y, int64_t(0))) * f.D8 + d];
     u = f.acc[2 * at], v = f.acc[2 * at + 1];
-#pragma unroll 4
+    w = f.rows[(f.by_token ? t0 + tk : max(y, int64_t(0))) * f.D8 + d];
+#pragma unroll 8
     for (int q = 1; q < f.slices; ++q) {
       const float4 a = f.acc[2 * (q * n + at)], b = f.acc[2 * (q * n + at) + 1];
       u.x += a.x, u.y += a.y, u.z += a.z, u.w += a.w;
       v.x += b.x, v.y += b.y, v.z += b.z, v.w += b.w;
     }
   };
-  if (threadIdx.x < items) gather(threadIdx.x);
-  float s = 0.0f;
-  if (in) {
-#pragma unroll 4
-    for (int i = i0; i < f.parts; i += kFinThreads / kFinTokens) {
-      const float q = f.part_sum[static_cast<int64_t>(i) * f.M + t];
-      const float r = f.part_max != nullptr ? f.part_max[static_cast<int64_t>(i) * f.M + t]
-                                            : f.refs[static_cast<int64_t>(f.piece_ref[i / f.piece_parts]) * f.M + t];
+  float ref, s = 0.0f;
+  if (f.part_max != nullptr) {
+    ref = z * kLog2e;
+#pragma unroll 8
+    for (int i = i0; i < f.parts; i += kStep) ref = fmaxf(ref, f.part_max[static_cast<int64_t>(i) * f.M + tc]);
+#pragma unroll
+    for (int o = 16; o >= kFinTokens; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+    if ((threadIdx.x & 31) < kFinTokens) red[warp][k] = ref;
+    __syncthreads();
+    for (int q = 0; q < kFinThreads / 32; ++q) ref = fmaxf(ref, red[q][k]);
+    __syncthreads();
+#pragma unroll 8
+    for (int i = i0; i < f.parts; i += kStep) {
+      const float q = f.part_sum[static_cast<int64_t>(i) * f.M + tc], r = f.part_max[static_cast<int64_t>(i) * f.M + tc];
       s += r == ref ? q : q == 0.0f ? 0.0f : q * exp2f(r - ref);
     }
+  } else {
+    // the first parts are on their way while the references and dx's first item are fetched
+    float q[kAt];
+#pragma unroll
+    for (int h = 0; h < kAt; ++h) {
+      const int i = i0 + h * kStep;
+      q[h] = i < f.parts ? f.part_sum[static_cast<int64_t>(i) * f.M + tc] : 0.0f;
+    }
+    ref = f.refs[static_cast<int64_t>(f.pieces) * f.M + tc];
+    if (threadIdx.x < items) gather(threadIdx.x);
+    auto add = [&](int i, float v) {     // one piece: its R is the last
+      if (f.pieces == 1) {
+        s += v;
+      } else {
+        const float r = f.refs[static_cast<int64_t>(i / f.piece_parts + 1) * f.M + tc];
+        s += r == ref ? v : v * exp2f(r - ref);
+      }
+    };
+#pragma unroll
+    for (int h = 0; h < kAt; ++h)
+      if (i0 + h * kStep < f.parts) add(i0 + h * kStep, q[h]);
+#pragma unroll 4
+    for (int i = i0 + kAt * kStep; i < f.parts; i += kStep) add(i, f.part_sum[static_cast<int64_t>(i) * f.M + tc]);
   }
 #pragma unroll
   for (int o = 16; o >= kFinTokens; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if ((threadIdx.x & 31) < kFinTokens) red[warp][k] = s;
   __syncthreads();
   if (threadIdx.x < kFinTokens) {
-    const bool live = in && f.clean[t] >= 0;
+    const bool live = in && yt >= 0;
     float others = 0.0f;
     for (int q = 0; q < kFinThreads / 32; ++q) others += red[q][k];
     const float d = fmaf(z, kLog2e, -ref);      // log2 of own
@@ -845,9 +765,9 @@ __global__ void __launch_bounds__(kFinThreads) lm_finish(const FinishArgs f) {
     const float total = others + own;
     // the quotient keeps the digits of a sure token's loss; far below the largest logit own vanishes
     const float l = d > -28.0f ? log1pf(others / own) : fmaf(-kLn2, d, logf(total));
-    const float g = !live ? 0.0f : f.gscale == nullptr ? 1.0f : f.gscale[f.gscale_per_row ? t : 0];
+    const float g = live ? g0 : 0.0f;
     coef[k] = make_float2(g / total, g * (others / total));
-    target[k] = live ? f.clean[t] : -1;
+    target[k] = live ? yt : -1;
     if (in && blockIdx.y == 0) {
       f.loss[t] = live ? l : 0.0f;
       if (f.lse != nullptr) f.lse[t] = live ? z + l : 0.0f;
@@ -874,158 +794,94 @@ __global__ void __launch_bounds__(kFinThreads) lm_finish(const FinishArgs f) {
 size_t a1024(size_t b) { return (b + 1023) & ~static_cast<size_t>(1023); }
 
 constexpr int64_t kBlockTokens = 8192;              // tokens of one pass over the vocabulary
-constexpr int64_t kPieceBytes = 128ll << 20;        // P of one piece at most (two are held)
+constexpr int64_t kPieceBytes = 256ll << 20;        // P of one piece
 
-// Clusters that are resident at once (one CTA an SM); looked up once per device.
-int max_clusters() {
-  constexpr int kMaxDev = 64;
-  static std::atomic<int> cache[kMaxDev];
-  int dev = 0;
-  cudaGetDevice(&dev);
-  const bool slot = dev >= 0 && dev < kMaxDev;
-  if (slot && cache[dev].load(std::memory_order_relaxed) > 0) return cache[dev].load(std::memory_order_relaxed);
-  int n = 0;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kCluster;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count() / kCluster * kCluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaFuncSetAttribute(lm_gemm<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, lm_gemm<true>, &cfg) != cudaSuccess || n < 1) {
-    cudaGetLastError();
-    return std::max(1, device_sm_count() / kCluster);    // sizes can be asked without a device
-  }
-  if (slot) cache[dev].store(n, std::memory_order_relaxed);
-  return n;
+// Vocabulary entries of a piece: P, and a stored head's decoded copy, stay within kPieceBytes, the pieces are about equal, and
+// each starts at a multiple of 256 (a whole tile; 256 stored rows of a multiple of 64 elements
+// are whole nested blocks of the NF4 format).
+int64_t piece_cols(int64_t M, int64_t V, int64_t D, bool stored, bool grad) {
+  int64_t fit = V + kTile;
+  if (grad) fit = std::max<int64_t>(kTile, kPieceBytes / (2 * M) / kTile * kTile);
+  if (stored) fit = std::max<int64_t>(kTile, std::min(fit, kPieceBytes / (2 * D)) / kTile * kTile);   // its decoded copy
+  const int64_t pieces = (V + fit - 1) / fit;
+  return ((V + pieces - 1) / pieces + kTile - 1) / kTile * kTile;
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int max_clusters() { return device_sm_count() / kCluster; }
 
-// How a block of M tokens runs: vocabulary tiles of a piece and parts of the gradient's
-// contraction.  Costs are in 128-deep steps of a cluster: for each piece the rounds of gradient
-// tiles (and 6 steps for each one's ends), then the scores, which even out what the gradient of
-// the piece before left uneven; a phase ends with the last score, so half a tile is lost there.
-struct LmPlan {
-  int piece_tiles, slices;
-};
-LmPlan lm_plan(int64_t M, int64_t V, int64_t D, bool stored, bool grad) {
-  const int64_t tiles = ceil_div(V, kTile), tt = ceil_div(M, kTile), td = ceil_div(D, kTile);
-  const int64_t d_steps = ceil_div(D, kStepK), n = max_clusters();
-  int64_t fit = std::max<int64_t>(1, kPieceBytes / (2 * tt * kTile) / kTile);
-  if (stored) fit = std::max<int64_t>(1, std::min(fit, 2 * kPieceBytes / (2 * D) / kTile));   // and its decoded copy
-  if (!grad) return LmPlan{static_cast<int>(std::min(fit, tiles)), 0};
-  LmPlan best{1, 1};
-  double best_cost = 1e300;
-  const int64_t fewest = ceil_div(tiles, fit);
-  for (int64_t pieces = fewest; pieces <= 2 * fewest && pieces <= tiles; ++pieces) {
-    const int64_t pt = ceil_div(tiles, pieces), last = tiles - (ceil_div(tiles, pt) - 1) * pt, count = ceil_div(tiles, pt);
-    for (int s = 1; s <= 16 && (s == 1 || last * 2 / s >= 8); ++s) {
-      const double g = static_cast<double>(ceil_div(pt * 2, s)) + 6.0;        // steps of a gradient tile
-      const int64_t grads = tt * td * s;
-      const double scores = static_cast<double>(tt * pt) / n * d_steps;
-      const double first = static_cast<double>(ceil_div(tt * pt, n)) * d_steps;
-      const double middle = std::max(static_cast<double>(grads) / n * g + scores + 0.5 * d_steps,
-                                     static_cast<double>(ceil_div(grads, n)) * g);
-      const double end = static_cast<double>(ceil_div(grads, n)) * (static_cast<double>(ceil_div(last * 2, s)) + 6.0);
-      // each further slice is fp32 sums read and written once more a piece: about 2 steps a round
-      const double cost = first + (count - 1) * (middle + 6.0) + end + count * (s - 1) * 2.0 * grads / n / s;
-      if (cost < best_cost * 0.995) best = LmPlan{static_cast<int>(pt), s}, best_cost = cost;
-    }
+// Parts of the gradient's contraction: enough that the tiles fill the SMs, each part at least
+// four steps long; of those up to 32 the one with the least rounds of steps (and 6 steps for a
+// tile's ends).
+int grad_slices(int64_t tiles, int64_t cols) {
+  const int64_t steps = (cols + kStepK - 1) / kStepK;
+  const int64_t n = max_clusters();
+  int best = 1;
+  double best_cost = 1e30;
+  for (int s = 1; s <= 32 && (s == 1 || steps / s >= 4); ++s) {
+    const int64_t rounds = (tiles * s + n - 1) / n;
+    const double cost = static_cast<double>(rounds) * (static_cast<double>((steps + s - 1) / s) + 6.0);
+    if (cost < best_cost * 0.97) best = s, best_cost = cost;
   }
   return best;
 }
 
 struct LmLayout {
-  int64_t Mb, cols, Mp;
-  int pieces, tiles, slices;
+  int64_t Mb, cols;
+  int pieces, tiles, slices, piece_tiles;
   bool stream;              // the logits come from lm_stream.cu
   int parts, piece_parts;   // sums a token has, in all and from one piece
-  size_t clean, zt, refs, piece_ref, spike, flags, any, arrived, part_sum, part_max, wy, wb, P, acc, total;
+  size_t clean, zt, refs, spike, flags, part_sum, part_max, wy, wb, P, acc, total;
   LmLayout(int64_t M, int64_t V, int64_t D, bool stored, bool grad) {
     Mb = std::min(M, kBlockTokens);
-    Mp = ceil_div(Mb, kTile) * kTile;
-    tiles = static_cast<int>(ceil_div(V, kTile));
-    // without a gradient a piece only bounds the decoded copy of a stored head
-    const LmPlan plan = grad || stored ? lm_plan(Mb, V, D, stored, grad) : LmPlan{tiles, 0};
-    cols = static_cast<int64_t>(plan.piece_tiles) * kTile;
-    slices = plan.slices;
-    pieces = static_cast<int>(ceil_div(tiles, plan.piece_tiles));
+    cols = piece_cols(Mb, V, D, stored, grad);
+    pieces = static_cast<int>((V + cols - 1) / cols);
+    piece_tiles = static_cast<int>(cols / kTile);
+    tiles = static_cast<int>((V + kTile - 1) / kTile);
     stream = Mb <= kLmStreamMaxM && D <= kLmStreamMaxD;
-    piece_parts = stream ? lm_stream_ctas() : 2 * plan.piece_tiles;
+    piece_parts = stream ? lm_stream_ctas() : 2 * piece_tiles;
     parts = stream ? pieces * piece_parts : 2 * tiles;
+    const int64_t tt = (Mb + kTile - 1) / kTile, ft = (D + kTile - 1) / kTile;
+    slices = grad ? grad_slices(tt * ft, V - (pieces - 1) * cols) : 0;   // the last piece is the smallest
     size_t off = 0;
     auto take = [&](size_t b) {
       const size_t at = off;
       off += a1024(b);
       return at;
     };
-    const size_t m = static_cast<size_t>(Mb), np = static_cast<size_t>(pieces);
+    const size_t m = static_cast<size_t>(Mb);
     clean = take(8 * m);
     zt = take(4 * m);
-    refs = take(grad ? 4 * m * (np + 1) : 0);
-    piece_ref = take(4 * np);
-    spike = take(grad ? 4 * m * np : 0);
-    flags = take(grad ? 4 * static_cast<size_t>(Mp / kTile) * np : 0);
-    any = take(4 * np);
-    arrived = take(4 * np);
+    refs = take(grad ? 4 * m * (pieces + 1) : 0);
+    spike = take(grad ? 4 * m * pieces : 0);
+    flags = take(grad ? sizeof(int) * static_cast<size_t>(tt) * pieces : 0);
     part_sum = take(4 * m * parts);
     part_max = take(grad ? 0 : 4 * m * parts);
     wy = take(stored ? 2 * (m + kSamples) * D : 0);
     wb = take(stored ? 2 * static_cast<size_t>(std::min(cols, V)) * D : 0);
-    P = take(grad ? 2 * 2 * static_cast<size_t>(Mp) * cols : 0);
+    P = take(grad ? 2 * m * cols : 0);
     acc = take(grad ? sizeof(float) * m * D * slices : 0);
     total = off;
   }
 };
 
-struct LmMaps {
-  CUtensorMap x, w, wg, p, pg;
-};
-
-// kGradient: a cooperative launch (its clusters wait for one another), unless it only takes the
-// gradient of a P that is there.
-template <bool kGradient>
-cudaError_t launch_lm_gemm(const LmParams& p, const LmMaps& m, cudaStream_t st) {
+template <int MODE>
+cudaError_t launch_lm_gemm(const LmParams& p, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& pm,
+                           cudaStream_t st) {
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(lm_gemm<kGradient>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    attr_err = cudaFuncSetAttribute(lm_gemm<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   });
   if (attr_err != cudaSuccess) return attr_err;
-  const int64_t scores = static_cast<int64_t>(p.tiles_t) * (p.cols / kTile);
-  const int64_t grads = kGradient ? static_cast<int64_t>(p.tiles_t) * p.tiles_d * p.slices : 0;
-  const int64_t clusters = std::min<int64_t>(std::max(p.make_scores ? scores : 0, grads), max_clusters());
+  const int64_t units = static_cast<int64_t>(p.tiles_t) * p.tiles_f * (MODE == kGrad ? p.slices : 1);
+  const int64_t clusters = std::min<int64_t>(units, max_clusters());
   LmParams q = p;
   const WaitSettings ws = take_wait_settings();
   q.wait_ns = ws.wait_ns;
   q.skip_stage0 = ws.skip_stage0;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kCluster;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  if (kGradient && p.make_scores) {
-    at[1].id = cudaLaunchAttributeCooperative;
-    at[1].val.cooperative = 1;
-  } else {
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-  }
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * kCluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
   note_launch();
-  return cudaLaunchKernelEx(&cfg, lm_gemm<kGradient>, m.x, m.w, m.wg, m.p, m.pg, q);
+  return launch_pdl(lm_gemm<MODE>, dim3(static_cast<unsigned>(clusters * kCluster)), dim3(kThreads), kSmemBytes, st,
+                    kCluster, a, b, pm, q);
 }
 
 }  // namespace
@@ -1042,6 +898,7 @@ cudaError_t lm_loss(const LmLossArgs& a, void* ws, int* status, cudaStream_t st)
   auto* zt = reinterpret_cast<float*>(w + L.zt);
   auto* refs = reinterpret_cast<float*>(w + L.refs);
   auto* spike = reinterpret_cast<float*>(w + L.spike);
+  auto* flags = reinterpret_cast<int*>(w + L.flags);
   auto* part_sum = reinterpret_cast<float*>(w + L.part_sum);
   auto* part_max = reinterpret_cast<float*>(w + L.part_max);
   auto* acc = reinterpret_cast<float*>(w + L.acc);
@@ -1052,6 +909,7 @@ cudaError_t lm_loss(const LmLossArgs& a, void* ws, int* status, cudaStream_t st)
   for (int64_t m0 = 0; m0 < a.M; m0 += L.Mb) {
     const int64_t M = std::min(L.Mb, a.M - m0);
     const char* x = static_cast<const char*>(a.x) + 2 * m0 * a.D;
+    const int tt = static_cast<int>((M + kTile - 1) / kTile);
     const void* rows = a.w16;
     const int f16 = a.f16 ? 1 : 0;
     if (stored) {
@@ -1063,42 +921,33 @@ cudaError_t lm_loss(const LmLossArgs& a, void* ws, int* status, cudaStream_t st)
           cudaSuccess)
         return e;
     }
-    LmParams p{};
-    p.M = M;
-    p.D = a.D;
-    p.V = a.V;
-    p.Mp = static_cast<int>(L.Mp);
-    p.cols = static_cast<int>(L.cols);
-    p.tiles_t = static_cast<int>(ceil_div(M, kTile));
-    p.tiles_d = static_cast<int>(ceil_div(a.D, kTile));
-    p.d_steps = static_cast<int>(ceil_div(a.D, kStepK));
-    p.slices = L.slices;
-    p.band = p.tiles_t > 8 && p.tiles_d > 8 ? 8 : 0;
-    p.piece_parts = L.piece_parts;
-    p.f16 = f16;
-    p.range = a.f16 ? kRangeF16 : kRangeBf16;
-    p.targets = clean;
-    p.refs = refs;
-    p.piece_ref = reinterpret_cast<int*>(w + L.piece_ref);
-    p.spike = spike;
-    p.flags = reinterpret_cast<int*>(w + L.flags);
-    p.any = reinterpret_cast<int*>(w + L.any);
-    p.arrived = reinterpret_cast<unsigned*>(w + L.arrived);
-    p.part_sum = part_sum;
-    p.part_max = part_max;
-    p.acc = acc;
-    p.status = status;
-    note_launch();
-    if ((e = launch_pdl(grad && a.f16 ? lm_prep<true> : lm_prep<false>, dim3(static_cast<unsigned>(M)), dim3(kPrepThreads),
-                        0, st, 1, reinterpret_cast<const uint4*>(x), static_cast<const uint4*>(rows), stored ? 1 : 0,
-                        a.targets + m0, M, a.V, a.ignore_index, D8, f16, clean, zt, grad ? refs : nullptr, spike, p.flags,
-                        p.any, p.arrived, p.piece_ref, grad ? L.pieces : 0, p.tiles_t, status)) != cudaSuccess)
-      return e;
-    // The pieces of a stored head are decoded one at a time, and a streamed piece's logits are a
-    // launch of their own; otherwise one launch takes them all.
-    const int step = stored || L.stream ? 1 : L.pieces;
-    for (int c = 0; c < L.pieces; c += step) {
-      const int64_t v0 = c * L.cols, cols = std::min(L.cols * step, a.V - v0);
+    PrepArgs pr{};
+    pr.M = M;
+    pr.V = a.V;
+    pr.D8 = D8;
+    pr.ignore = a.ignore_index;
+    pr.x = reinterpret_cast<const uint4*>(x);
+    pr.rows = static_cast<const uint4*>(rows);
+    pr.by_token = stored ? 1 : 0;
+    pr.f16 = f16;
+    pr.targets = a.targets + m0;
+    pr.clean = clean;
+    pr.zt = zt;
+    pr.ref = grad ? refs : nullptr;
+    pr.spike = spike;
+    pr.flags = flags;
+    pr.pieces = grad ? L.pieces : 0;
+    pr.tiles_t = tt;
+    if (grad || L.stream) {
+      note_launch();
+      if ((e = launch_pdl(grad && a.f16 ? lm_prep<true> : lm_prep<false>,
+                          dim3(static_cast<unsigned>(M)), dim3(kPrepWarps * 32), 0, st, 1, pr, status)) != cudaSuccess)
+        return e;
+    }
+    CUtensorMap xm;
+    if (!make_map(&xm, dt, x, a.D, M, 2 * a.D, kSub, kHalf, sw)) return cudaErrorInvalidValue;
+    for (int c = 0; c < L.pieces; ++c) {
+      const int64_t v0 = c * L.cols, cols = std::min(L.cols, a.V - v0);
       const void* wc = static_cast<const char*>(a.w16) + 2 * v0 * a.D;
       if (stored) {
         Nf4View part = a.W;
@@ -1110,20 +959,38 @@ cudaError_t lm_loss(const LmLossArgs& a, void* ws, int* status, cudaStream_t st)
         wc = w + L.wb;
         if ((e = launch_dequantize(part, w + L.wb, a.f16 ? NF4_F16 : NF4_BF16, st)) != cudaSuccess) return e;
       }
-      LmMaps m;
-      bool ok = make_map(&m.x, dt, x, a.D, M, 2 * a.D, kSub, kHalf, sw);
-      ok = ok && make_map(&m.w, dt, wc, a.D, cols, 2 * a.D, kSub, kHalf, sw);
-      m.wg = m.p = m.pg = m.w;
+      CUtensorMap wm, wg, pm, pg;
+      bool ok = make_map(&wm, dt, wc, a.D, cols, 2 * a.D, kSub, kHalf, sw);
       if (grad) {
-        ok = ok && make_map(&m.wg, dt, wc, a.D, cols, 2 * a.D, kSub, kSub, sw);
-        ok = ok && make_map(&m.p, dt, w + L.P, L.cols, 2 * L.Mp, 2 * L.cols, kBoxCols, 32, CU_TENSOR_MAP_SWIZZLE_64B);
-        ok = ok && make_map(&m.pg, dt, w + L.P, L.cols, 2 * L.Mp, 2 * L.cols, kSub, kHalf, sw);
+        ok = ok && make_map(&wg, dt, wc, a.D, cols, 2 * a.D, kSub, kSub, sw);
+        ok = ok && make_map(&pm, dt, w + L.P, L.cols, M, 2 * L.cols, kBoxCols, 32,
+                            CU_TENSOR_MAP_SWIZZLE_64B);
+        ok = ok && make_map(&pg, dt, w + L.P, L.cols, M, 2 * L.cols, kSub, kHalf, sw);
+      } else {
+        wg = pm = pg = wm;
       }
       if (!ok) return cudaErrorInvalidValue;
-      p.c0 = c;
-      p.c1 = c + step;
-      p.w_row0 = static_cast<int>(v0);
-      p.make_scores = L.stream ? 0 : 1;
+      LmParams p{};
+      p.M = M;
+      p.D = a.D;
+      p.cols = cols;
+      p.v0 = v0;
+      p.red_len = a.D;
+      p.red_steps = static_cast<int>((a.D + kStepK - 1) / kStepK);
+      p.tiles_t = tt;
+      p.tiles_f = static_cast<int>((cols + kTile - 1) / kTile);
+      p.slices = 1;
+      p.f16 = a.f16 ? 1 : 0;
+      p.range = a.f16 ? kRangeF16 : kRangeBf16;
+      p.prep = pr;
+      p.prepare = c == 0 ? 1 : 0;
+      p.status = status;
+      p.part_sum = part_sum + static_cast<int64_t>(c) * L.piece_parts * M;
+      p.part_max = part_max + static_cast<int64_t>(c) * L.piece_parts * M;
+      p.ref = refs + static_cast<int64_t>(c) * M;
+      p.ref_next = refs + static_cast<int64_t>(c + 1) * M;
+      p.spike = spike + static_cast<int64_t>(c) * M;
+      p.flags = flags + static_cast<int64_t>(c) * tt;
       if (L.stream) {
         LmStreamArgs q{};
         q.M = static_cast<int>(M);
@@ -1134,20 +1001,34 @@ cudaError_t lm_loss(const LmLossArgs& a, void* ws, int* status, cudaStream_t st)
         q.W = wc;
         q.targets = clean;
         q.range = p.range;
-        q.ref = refs + static_cast<int64_t>(c) * M;
-        q.ref_next = refs + static_cast<int64_t>(c + 1) * M;
-        q.spike = spike + static_cast<int64_t>(c) * M;
-        q.flags = p.flags + static_cast<int64_t>(c) * p.tiles_t;
-        q.P = w + L.P + 2 * (c & 1) * L.Mp * L.cols;
+        q.ref = p.ref;
+        q.ref_next = p.ref_next;
+        q.spike = p.spike;
+        q.flags = p.flags;
+        q.P = w + L.P;
         q.ldp = L.cols;
-        q.part_sum = part_sum + static_cast<int64_t>(c) * L.piece_parts * M;
-        q.part_max = part_max + static_cast<int64_t>(c) * L.piece_parts * M;
+        q.part_sum = p.part_sum;
+        q.part_max = p.part_max;
         if ((e = launch_lm_stream(q, grad, a.f16, st)) != cudaSuccess) return e;
-        if (!grad) continue;
         q.redo = 1;
-        if ((e = launch_lm_stream(q, true, a.f16, st)) != cudaSuccess) return e;
+        if (grad && (e = launch_lm_stream(q, true, a.f16, st)) != cudaSuccess) return e;
+      } else if (!grad) {
+        if ((e = launch_lm_gemm<kMax>(p, xm, wm, pm, st)) != cudaSuccess) return e;
+      } else {
+        if ((e = launch_lm_gemm<kScores>(p, xm, wm, pm, st)) != cudaSuccess) return e;
+        p.redo = 1;
+        if ((e = launch_lm_gemm<kScores>(p, xm, wm, pm, st)) != cudaSuccess) return e;
       }
-      if ((e = grad ? launch_lm_gemm<true>(p, m, st) : launch_lm_gemm<false>(p, m, st)) != cudaSuccess) return e;
+      if (!grad) continue;
+      LmParams g = p;
+      g.red_len = cols;
+      g.red_steps = static_cast<int>((cols + kStepK - 1) / kStepK);
+      g.tiles_f = static_cast<int>((a.D + kTile - 1) / kTile);
+      g.slices = L.slices;
+      g.band = g.tiles_t > 8 && g.tiles_f > 8 ? 8 : 0;
+      g.add = c > 0 ? 1 : 0;
+      g.acc = acc;
+      if ((e = launch_lm_gemm<kGrad>(g, wg, pg, pm, st)) != cudaSuccess) return e;
     }
     FinishArgs f{};
     f.M = M;
@@ -1155,7 +1036,6 @@ cudaError_t lm_loss(const LmLossArgs& a, void* ws, int* status, cudaStream_t st)
     f.part_sum = part_sum;
     f.part_max = grad ? nullptr : part_max;
     f.refs = refs;
-    f.piece_ref = p.piece_ref;
     f.parts = L.parts;
     f.piece_parts = L.piece_parts;
     f.pieces = L.pieces;
