@@ -1,7 +1,7 @@
 // 8-bit activation checkpoints: storing, reading back, and the adapter gradient
 // dA = s G^T x taken straight from the codes.
 #include <algorithm>
-#include <mutex>
+#include <atomic>
 #include <type_traits>
 
 #include "mma_sync.cuh"
@@ -133,16 +133,20 @@ constexpr int kGradRanks = 16;
 constexpr int kGradWarps = 4;                                  // one block of 128 features each
 constexpr int kGradThreads = kGradWarps * 32;
 constexpr int kGradCols = kGradWarps * kActBlock;
-constexpr int kGradCtas = 4;                                   // resident on an SM
+constexpr int kGradCtas = 3;                                   // resident on an SM at most
 constexpr int kCodePitch = kGradCols + 32;                     // bytes: 4 rows x 32 bytes on 32 banks
 constexpr int kGPitch = 24;                                    // floats: 4 rows x 8 ranks on 32 banks
 constexpr int kRingCodes = 16 * kCodePitch, kRingG = 16 * kGPitch * 4, kRingS = 16 * kGradWarps * 4;
 constexpr int kRingBytes = kRingCodes + kRingG + kRingS;       // 10496
-constexpr int kRing = 5;
-constexpr int kGradSmem = kRing * kRingBytes;
 constexpr int kSumPitch = kGradCols + 4;                       // floats
 constexpr int kClusterMax = 16;
-static_assert(kGradRanks * kSumPitch * 4 <= kGradSmem, "a CTA's sums take the ring's place");
+// Stages of the ring and shared memory where k CTAs are meant to share an SM.  The memory is asked
+// for so that k + 1 do not fit: a launch that starts while the one before it ends would otherwise
+// fill the SMs that are free first and leave others without work.
+constexpr int ring_stages(int k) { return k == 1 ? 11 : k == 2 ? 7 : 5; }
+constexpr int grad_smem(int k) { return (k == 1 ? 116 : k == 2 ? 78 : 58) * 1024; }
+static_assert(ring_stages(1) * kRingBytes <= grad_smem(1) && ring_stages(2) * kRingBytes <= grad_smem(2) &&
+              ring_stages(3) * kRingBytes <= grad_smem(3) && kGradRanks * kSumPitch * 4 <= grad_smem(3), "the ring fits");
 
 // 16 (or 4) bytes to shared memory, of which the last 16 - n (4 - n) are zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
@@ -169,7 +173,7 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return r;
 }
 
-template <bool kVec>
+template <bool kVec, int kRing>
 __global__ void __launch_bounds__(kGradThreads, kGradCtas)
 act8_grad(const ActGradArgs a, int slice_steps, int cluster, int clusters, float* part) {
   extern __shared__ __align__(16) uint8_t ring[];
@@ -304,23 +308,29 @@ act8_grad(const ActGradArgs a, int slice_steps, int cluster, int clusters, float
       }
     }
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      uint32_t t[4];
+    for (int w2 = 0; w2 < 4; w2 += 2) {
+      // 8 products' fragments, then their hi halves and their lo halves: the two that add to the same
+      // sums stand 8 apart
+      uint32_t b[8][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) t[i] = w == 0 ? code[i].x : w == 1 ? code[i].y : w == 2 ? code[i].z : code[i].w;
-      // columns 4w, 4w + 1 of tokens 0 1 and 2 3, then columns 4w + 2, 4w + 3
+      for (int w = w2; w < w2 + 2; ++w) {
+        uint32_t t[4];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint32_t sel = c == 0 ? 0x5410u : 0x7632u;
-        const uint32_t x01 = __byte_perm(t[0], t[1], sel), x23 = __byte_perm(t[2], t[3], sel);
-        const uint32_t b00 = codes_half2<false>(x01), b01 = codes_half2<false>(x23);
-        const uint32_t b10 = codes_half2<true>(x01), b11 = codes_half2<true>(x23);
-        const int n = 4 * w + 2 * c;
-        mma16816<true>(acc[n], hi[0], hi[1], hi[2], hi[3], b00, b01);
-        mma16816<true>(acc[n + 1], hi[0], hi[1], hi[2], hi[3], b10, b11);
-        mma16816<true>(acc[n], lo[0], lo[1], lo[2], lo[3], b00, b01);
-        mma16816<true>(acc[n + 1], lo[0], lo[1], lo[2], lo[3], b10, b11);
+        for (int i = 0; i < 4; ++i) t[i] = w == 0 ? code[i].x : w == 1 ? code[i].y : w == 2 ? code[i].z : code[i].w;
+        // columns 4w, 4w + 1 of tokens 0 1 and 2 3, then columns 4w + 2, 4w + 3
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t sel = c == 0 ? 0x5410u : 0x7632u;
+          const uint32_t x01 = __byte_perm(t[0], t[1], sel), x23 = __byte_perm(t[2], t[3], sel);
+          const int n = 4 * (w - w2) + 2 * c;
+          b[n][0] = codes_half2<false>(x01), b[n][1] = codes_half2<false>(x23);
+          b[n + 1][0] = codes_half2<true>(x01), b[n + 1][1] = codes_half2<true>(x23);
+        }
       }
+#pragma unroll
+      for (int n = 0; n < 8; ++n) mma16816<true>(acc[4 * w2 + n], hi[0], hi[1], hi[2], hi[3], b[n][0], b[n][1]);
+#pragma unroll
+      for (int n = 0; n < 8; ++n) mma16816<true>(acc[4 * w2 + n], lo[0], lo[1], lo[2], lo[3], b[n][0], b[n][1]);
     }
   }
   // acc[n][k]: rank g + 8 (k / 2), feature 32 q + 16 (k % 2) + n of the warp's block, times 2^e
@@ -398,44 +408,82 @@ __global__ void act8_grad_finish(const ActGradArgs a, const float* part, int sli
   for (int k = 0; k < kW; ++k) a.dA[i + k] = v[k] * a.s * (a.weight != nullptr ? a.weight[kk + k] : 1.0f);
 }
 
-// Slices of the tokens, as clusters of CTAs: the counts with the least time, in units of a quarter
-// of a step: rounds of resident CTAs times their steps and 4 steps' worth for a CTA's own ends, 2
-// for a cluster's sums and one for every 8 CTAs of it, and with several clusters 10 for the launch
-// that adds them and a quarter for reading each.
+using GradKernel = void (*)(const ActGradArgs, int, int, int, float*);
+GradKernel grad_kernel(bool vec, int k) {
+  static const GradKernel table[2][kGradCtas] = {
+      {act8_grad<false, ring_stages(1)>, act8_grad<false, ring_stages(2)>, act8_grad<false, ring_stages(3)>},
+      {act8_grad<true, ring_stages(1)>, act8_grad<true, ring_stages(2)>, act8_grad<true, ring_stages(3)>}};
+  return table[vec ? 1 : 0][k - 1];
+}
+
+// Clusters of c CTAs that are resident at once with k CTAs an SM (clusters stay within a group of SMs,
+// so large ones leave some unused); looked up once per device.
+int resident_clusters(int c, int k) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> cache[kMaxDev][kClusterMax + 1][kGradCtas + 1];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool slot = dev >= 0 && dev < kMaxDev;
+  if (slot && cache[dev][c][k].load(std::memory_order_relaxed) > 0) return cache[dev][c][k].load(std::memory_order_relaxed);
+  int n = 0;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(c);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(c * 1024));
+  cfg.blockDim = dim3(kGradThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(grad_smem(k));
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const GradKernel f = grad_kernel(true, k);
+  if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, grad_smem(k)) != cudaSuccess ||
+      cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, f, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return std::max(1, device_sm_count() * k / c);    // sizes can be asked without a device
+  }
+  if (slot && n > 0) cache[dev][c][k].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Slices of the tokens, as `clusters` clusters of `cluster` CTAs, k CTAs an SM: the counts with the
+// least time in nanoseconds.  A step takes 420 ns where a CTA has an SM to itself, 580 with two and
+// 820 with three (measured at 4096 x 14336: 28 us for 5 slices, 22 for a cluster of 10); a CTA's
+// ends 3 us, a cluster's sums 1 us, the launch that adds several clusters 4 us.
 struct GradPlan {
-  int cluster, clusters;
+  int cluster, clusters, k;
   int64_t per;      // steps of a slice
 };
 GradPlan grad_plan(int64_t M, int64_t K, int r) {
   const int64_t groups = (K + kGradCols - 1) / kGradCols * ((r + kGradRanks - 1) / kGradRanks);
-  const int64_t steps = (M + 15) / 16, slots = kGradCtas * static_cast<int64_t>(device_sm_count());
-  GradPlan best{1, 1, steps};
-  int64_t best_cost = INT64_MAX;
+  const int64_t steps = (M + 15) / 16, sms = device_sm_count();
+  constexpr int kStepNs[kGradCtas + 1] = {0, 420, 580, 820};
+  GradPlan best{1, 1, 1, steps};
+  int64_t best_ns = INT64_MAX;
   for (int n = 1; n <= 8; ++n)
     for (int c = 1; c <= kClusterMax && n * c <= std::max<int64_t>(steps, 1); ++c) {
       const int64_t per = (steps + n * c - 1) / (n * c);
-      const int64_t rounds = (groups * n * c + slots - 1) / slots;
-      // CTAs that share an SM share its issue slots: a lone one runs its steps about 2.5 times as fast
-      const int64_t sharing = std::min<int64_t>(kGradCtas, (groups * n * c + device_sm_count() - 1) / device_sm_count());
-      const int64_t cost = rounds * (per * (1 + sharing) * 4 / (1 + kGradCtas) + 16) + (c > 1 ? 8 + c / 2 : 0) + (n > 1 ? 40 + n : 0);
-      if (cost < best_cost) best = GradPlan{c, n, per}, best_cost = cost;
+      const int k = static_cast<int>(std::min<int64_t>(kGradCtas, (groups * n * c + sms - 1) / sms));
+      const int fit = resident_clusters(c, k);
+      if (fit < 1) continue;
+      const int64_t waves = (groups * n + fit - 1) / fit;
+      const int64_t ns = waves * (per * kStepNs[k] + 3000) + (c > 1 ? 1000 : 0) + (n > 1 ? 4000 + 100 * n : 0);
+      if (ns < best_ns) best = GradPlan{c, n, k, per}, best_ns = ns;
     }
   return best;
 }
 
-template <bool kVec>
 cudaError_t launch_grad(const ActGradArgs& a, const GradPlan& g, float* part, cudaStream_t st) {
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [&] {
-    err = cudaFuncSetAttribute(act8_grad<kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
-    if (err == cudaSuccess) err = cudaFuncSetAttribute(act8_grad<kVec>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  });
-  if (err != cudaSuccess) return err;
+  const GradKernel f = grad_kernel(a.K % 16 == 0, g.k);
+  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, grad_smem(g.k));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
   note_launch();
   const dim3 grid(static_cast<unsigned>(g.cluster * g.clusters), static_cast<unsigned>((a.K + kGradCols - 1) / kGradCols),
                   static_cast<unsigned>((a.r + kGradRanks - 1) / kGradRanks));
-  return launch_pdl(act8_grad<kVec>, grid, dim3(kGradThreads), kGradSmem, st, static_cast<unsigned>(g.cluster), a,
+  return launch_pdl(f, grid, dim3(kGradThreads), static_cast<size_t>(grad_smem(g.k)), st, static_cast<unsigned>(g.cluster), a,
                     static_cast<int>(g.per), g.cluster, g.clusters, part);
 }
 
@@ -476,7 +524,7 @@ cudaError_t launch_act8_grad(const ActGradArgs& a, void* ws, cudaStream_t st) {
   if (a.M == 0) return cudaMemsetAsync(a.dA, 0, sizeof(float) * static_cast<size_t>(a.r) * a.K, st);
   const GradPlan g = grad_plan(a.M, a.K, a.r);
   auto* part = static_cast<float*>(ws);
-  const cudaError_t e = a.K % 16 == 0 ? launch_grad<true>(a, g, part, st) : launch_grad<false>(a, g, part, st);
+  const cudaError_t e = launch_grad(a, g, part, st);
   if (e != cudaSuccess || g.clusters == 1) return e;
   const int w = a.K % 4 == 0 ? 4 : 1;
   const int64_t n = static_cast<int64_t>(a.r) * a.K / w;
