@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(512) rms_norm_bwd(const NormBwdArgs a) {
 
 // Workers walk over rows: G threads a worker, blockDim.x / G workers a CTA.  kCk: n comes from the
 // checkpoint (K % 16 == 0: whole 16-byte pieces of codes), else from h.
-template <typename T, bool kCk, bool kDw>
+template <typename T, int kN, bool kCk, bool kDw>
 __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, int G, int stages, int* status) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[2 * 32];
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, in
   const int64_t workers = static_cast<int64_t>(gridDim.x) * (blockDim.x / G);
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (blockDim.x / G) + w;
   const int64_t nb = (a.K + kActBlock - 1) / kActBlock;
-  const int64_t blk = min(static_cast<int64_t>(t / (kActLanes / kRingN)), nb - 1);
+  const int64_t blk = min(static_cast<int64_t>(t / (kActLanes / kN)), nb - 1);
   const float invK = 1.0f / static_cast<float>(a.K);
   auto issue = [&](int64_t m, int s) {
     if (m >= a.M) return;
@@ -169,9 +169,9 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, in
   };
   if (t == 0)
     for (int s = 0; s < stages; ++s) issue(first + s * workers, s);
-  float dw[kRingN][8];
+  float dw[kN][8];
 #pragma unroll
-  for (int u = 0; u < kRingN; ++u)
+  for (int u = 0; u < kN; ++u)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[u][j] = 0.0f;
   // the row's rstd and the block's scale, one row ahead
@@ -187,11 +187,11 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, in
     }
     tc::mbar_wait(bar_at + 8 * s, ph, &gave_up, status);   // see rms_norm_fwd_ring
     const uint8_t* stage = ring + s * bytes;
-    float g[kRingN][8], n[kRingN][8];
+    float g[kN][8], n[kN][8];
     float sum = 0.0f;
 #pragma unroll
-    for (int u = 0; u < kRingN; ++u) {
-      const int64_t c = chunk_of(t, kRingN, u);
+    for (int u = 0; u < kN; ++u) {
+      const int64_t c = chunk_of(t, kN, u);
       float wt[8];
       load8<float, true>(a.weight, c, a.K, wt);
       ring8<T>(stage, c, a.K, g[u]);
@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, in
     }
     const float mean = worker_sum(sum, G, red, turn) * invK;
 #pragma unroll
-    for (int u = 0; u < kRingN; ++u) {
-      const int64_t c = chunk_of(t, kRingN, u);
+    for (int u = 0; u < kN; ++u) {
+      const int64_t c = chunk_of(t, kN, u);
       float o[8];
       if (a.dresidual != nullptr) ring8<T>(stage + row_bytes + saved_bytes, c, a.K, o);
 #pragma unroll
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, in
   if (kDw) {
     float* part = a.partial + first * a.K;
 #pragma unroll
-    for (int u = 0; u < kRingN; ++u) store8<float, true>(part, chunk_of(t, kRingN, u), a.K, dw[u]);
+    for (int u = 0; u < kN; ++u) store8<float, true>(part, chunk_of(t, kN, u), a.K, dw[u]);
   }
 }
 
@@ -250,6 +250,7 @@ __global__ void norm_dweight(const float* part, int64_t P, int64_t K, float* dwe
   const int64_t k = static_cast<int64_t>(blockIdx.x) * kDwCols + threadIdx.x;
   float s = 0.0f;
   if (k < K)
+#pragma unroll 8
     for (int64_t q = threadIdx.y; q < P; q += kDwRows) s += part[q * K + k];
   red[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
@@ -276,23 +277,29 @@ BwdShape bwd_shape(int64_t M, int64_t K) {
   return b;
 }
 
+// Chunks a thread of the ring's workers holds; 0: the rows are loaded by their threads.  With dweight's
+// sums beside a row's dn and n, four are more than its registers (4096 x 4096: 42 us with four, 32 with
+// two); short rows have so many workers that adding up their sums costs more than the ring gains
+// (4096 x 576: 14 us, loaded by the threads 11; 4096 x 2048: 20 and 22).
+int ring_chunks(int64_t K, bool dw) { return !dw ? 4 : K <= 1024 ? 0 : K <= 8192 ? 2 : 4; }
+
 // The ring's shape for a call, from what a row's inputs take (an element of `elem` bytes).
-RingShape bwd_ring(int64_t M, int64_t K, size_t elem, bool ck, bool dres) {
-  if (K % (ck ? 16 : 8) != 0) return RingShape{};
-  return ring_shape(M, K, K * elem * (dres ? 2 : 1) + K * (ck ? 1 : elem), 128);
+RingShape bwd_ring(int64_t M, int64_t K, size_t elem, bool ck, bool dres, int n) {
+  if (n == 0 || K % (ck ? 16 : 8) != 0) return RingShape{};
+  return ring_shape(M, K, K * elem * (dres ? 2 : 1) + K * (ck ? 1 : elem), n == 4 ? 128 : 104, n);
 }
 
-template <typename T, bool kCk, bool kDw>
+template <typename T, int kN, bool kCk, bool kDw>
 cudaError_t launch_ring(const NormBwdArgs& a, const RingShape& r, int* status, cudaStream_t st) {
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
   std::call_once(once, [&] {
-    err = cudaFuncSetAttribute(rms_norm_bwd_ring<T, kCk, kDw>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    err = cudaFuncSetAttribute(rms_norm_bwd_ring<T, kN, kCk, kDw>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(kRingSmemMax));
   });
   if (err != cudaSuccess) return err;
   note_launch();
-  return launch_pdl(rms_norm_bwd_ring<T, kCk, kDw>, dim3(r.grid), dim3(r.G * r.workers), r.smem, st, 1, a, r.G, r.stages,
+  return launch_pdl(rms_norm_bwd_ring<T, kN, kCk, kDw>, dim3(r.grid), dim3(r.G * r.workers), r.smem, st, 1, a, r.G, r.stages,
                     status);
 }
 
@@ -306,9 +313,13 @@ template <typename T, bool kVec, bool kDw>
 cudaError_t launch(const NormBwdArgs& a, int* status, cudaStream_t st) {
   if (kVec) {
     const bool ck = a.h == nullptr;
-    const RingShape r = bwd_ring(a.M, a.K, sizeof(T), ck, a.dresidual != nullptr);
+    const int n = ring_chunks(a.K, kDw);
+    const RingShape r = bwd_ring(a.M, a.K, sizeof(T), ck, a.dresidual != nullptr, n);
     if (r.stages > 0) {
-      const cudaError_t e = ck ? launch_ring<T, true, kDw>(a, r, status, st) : launch_ring<T, false, kDw>(a, r, status, st);
+      constexpr int kFew = kDw ? 2 : 4;
+      const cudaError_t e = n == 4 ? (ck ? launch_ring<T, 4, true, kDw>(a, r, status, st) : launch_ring<T, 4, false, kDw>(a, r, status, st))
+                                   : (ck ? launch_ring<T, kFew, true, kDw>(a, r, status, st)
+                                         : launch_ring<T, kFew, false, kDw>(a, r, status, st));
       if (e != cudaSuccess || !kDw) return e;
       return add_groups(a, std::min<int64_t>(static_cast<int64_t>(r.grid) * r.workers, a.M), st);
     }
@@ -344,7 +355,7 @@ size_t rms_norm_bwd_ws_bytes(int64_t M, int64_t K) {
   for (const size_t elem : {sizeof(float), sizeof(__half)})
     for (const bool ck : {false, true})
       for (const bool dres : {false, true}) {
-        const RingShape r = bwd_ring(M, K, elem, ck, dres);
+        const RingShape r = bwd_ring(M, K, elem, ck, dres, ring_chunks(K, true));
         if (r.stages > 0) groups = std::max<int64_t>(groups, static_cast<int64_t>(r.grid) * r.workers);
       }
   return sizeof(float) * static_cast<size_t>(groups) * static_cast<size_t>(K);

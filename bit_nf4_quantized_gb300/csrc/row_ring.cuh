@@ -1,6 +1,6 @@
 // Rows streamed through shared memory for the norm's kernels: a worker (one warp, or a whole CTA)
 // walks over rows, each row's inputs arrive by bulk copies in a ring of stages, and every thread
-// holds four chunks of one block of the row in registers (train_ops.cuh).  The copies need no
+// holds four (or two) chunks of one block of the row in registers (train_ops.cuh).  The copies need no
 // registers and stay in flight across the reductions, which is what keeps HBM busy.
 #pragma once
 
@@ -9,7 +9,7 @@
 
 namespace qnf4 {
 
-constexpr int kRingN = 4;                        // chunks a thread holds
+constexpr int kRingN = 4;                        // chunks a thread holds, where nothing else is said
 constexpr int kRingStagesMax = 4;
 constexpr size_t kRingSmemMax = 200 * 1024;      // a CTA's ring at most; two stages must fit
 constexpr int kRingWarpWorkers = 4;              // workers of a CTA where a worker is a warp
@@ -27,9 +27,9 @@ struct RingShape {
   unsigned grid;
   size_t smem;
 };
-inline RingShape ring_shape(int64_t M, int64_t K, size_t bytes, int regs) {
+inline RingShape ring_shape(int64_t M, int64_t K, size_t bytes, int regs, int n = kRingN) {
   RingShape s{};
-  const int64_t lanes = (K + kActBlock - 1) / kActBlock * (kActLanes / kRingN);
+  const int64_t lanes = (K + kActBlock - 1) / kActBlock * (kActLanes / n);
   if (lanes < 16 || lanes > 512) return s;   // under half a warp busy, or over the registers
   s.G = static_cast<int>((lanes + 31) / 32 * 32);
   s.workers = s.G == 32 ? kRingWarpWorkers : 1;
