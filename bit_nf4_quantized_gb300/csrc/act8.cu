@@ -1,7 +1,7 @@
 // 8-bit activation checkpoints: storing, reading back, and the adapter gradient
 // dA = s G^T x taken straight from the codes.
 #include <algorithm>
-#include <atomic>
+#include <mutex>
 #include <type_traits>
 
 #include "mma_sync.cuh"
@@ -140,6 +140,9 @@ constexpr int kRingCodes = 16 * kCodePitch, kRingG = 16 * kGPitch * 4, kRingS = 
 constexpr int kRingBytes = kRingCodes + kRingG + kRingS;       // 10496
 constexpr int kSumPitch = kGradCols + 4;                       // floats
 constexpr int kClusterMax = 16;
+// steps between the additions of a slice's sums in fp32 registers: the tensor cores truncate as they add
+// (26 steps: 8e-7 of dA in norm, twice as many twice that)
+constexpr int kSliceSteps = 26;
 // Stages of the ring and shared memory where k CTAs are meant to share an SM.  The memory is asked
 // for so that k + 1 do not fit: a launch that starts while the one before it ends would otherwise
 // fill the SMs that are free first and leave others without work.
@@ -173,8 +176,9 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return r;
 }
 
-template <bool kVec, int kRing>
-__global__ void __launch_bounds__(kGradThreads, kGradCtas)
+// kLong: slices of more than kSliceSteps steps, whose sums move on to other registers that often.
+template <bool kVec, int kRing, bool kLong>
+__global__ void __launch_bounds__(kGradThreads, kLong ? 2 : kGradCtas)
 act8_grad(const ActGradArgs a, int slice_steps, int cluster, int clusters, float* part) {
   extern __shared__ __align__(16) uint8_t ring[];
   pdl_allow_next();
@@ -250,7 +254,14 @@ act8_grad(const ActGradArgs a, int slice_steps, int cluster, int clusters, float
   for (int i = 0; i < 16; ++i)
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
-  int e = 126;
+  float sum[kLong ? 16 : 1][4];
+  if (kLong) {
+#pragma unroll
+    for (int i = 0; i < (kLong ? 16 : 1); ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum[i][k] = 0.0f;
+  }
+  int e = 126, since = 0;
   for (int st = 0; st < kRing - 1; ++st) issue(st, st);
   int slot = 0;
   for (int st = 0; st < n_steps; ++st, slot = slot + 1 == kRing ? 0 : slot + 1) {
@@ -277,7 +288,10 @@ act8_grad(const ActGradArgs a, int slice_steps, int cluster, int clusters, float
 #pragma unroll
       for (int i = 0; i < 16; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[i][k] *= f;
+        for (int k = 0; k < 4; ++k) {
+          acc[i][k] *= f;
+          if (kLong) sum[kLong ? i : 0][k] *= f;
+        }
     }
     const float up = __int_as_float((e + 127) << 23);
     uint32_t hi[4], lo[4];     // a0: rank g, the lane's tokens 0 1; a1: rank g + 8; a2, a3: tokens 2 3
@@ -332,6 +346,19 @@ act8_grad(const ActGradArgs a, int slice_steps, int cluster, int clusters, float
 #pragma unroll
       for (int n = 0; n < 8; ++n) mma16816<true>(acc[4 * w2 + n], lo[0], lo[1], lo[2], lo[3], b[n][0], b[n][1]);
     }
+    if (kLong && ++since == kSliceSteps) {
+      since = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[kLong ? i : 0][k] += acc[i][k], acc[i][k] = 0.0f;
+    }
+  }
+  if (kLong) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i][k] += sum[kLong ? i : 0][k];
   }
   // acc[n][k]: rank g + 8 (k / 2), feature 32 q + 16 (k % 2) + n of the warp's block, times 2^e
   const float back = __int_as_float((127 - e) << 23);
@@ -409,43 +436,60 @@ __global__ void act8_grad_finish(const ActGradArgs a, const float* part, int sli
 }
 
 using GradKernel = void (*)(const ActGradArgs, int, int, int, float*);
-GradKernel grad_kernel(bool vec, int k) {
-  static const GradKernel table[2][kGradCtas] = {
-      {act8_grad<false, ring_stages(1)>, act8_grad<false, ring_stages(2)>, act8_grad<false, ring_stages(3)>},
-      {act8_grad<true, ring_stages(1)>, act8_grad<true, ring_stages(2)>, act8_grad<true, ring_stages(3)>}};
-  return table[vec ? 1 : 0][k - 1];
+GradKernel grad_kernel(bool vec, bool is_long, int k) {
+  static const GradKernel table[2][2][kGradCtas] = {
+      {{act8_grad<false, ring_stages(1), false>, act8_grad<false, ring_stages(2), false>, act8_grad<false, ring_stages(3), false>},
+       {act8_grad<false, ring_stages(1), true>, act8_grad<false, ring_stages(2), true>, nullptr}},
+      {{act8_grad<true, ring_stages(1), false>, act8_grad<true, ring_stages(2), false>, act8_grad<true, ring_stages(3), false>},
+       {act8_grad<true, ring_stages(1), true>, act8_grad<true, ring_stages(2), true>, nullptr}}};
+  return table[vec ? 1 : 0][is_long ? 1 : 0][k - 1];
 }
 
-// Clusters of c CTAs that are resident at once with k CTAs an SM (clusters stay within a group of SMs,
-// so large ones leave some unused); looked up once per device.
-int resident_clusters(int c, int k) {
+// Clusters of c CTAs that are resident at once with k CTAs an SM: clusters stay within a group of SMs, so
+// large ones leave some unused.  Filled once per device, with the kernels' attributes.
+constexpr int kClusterSizes[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16};
+struct Residency {
+  int sms;
+  int clusters[kGradCtas + 1][kClusterMax + 1];
+};
+cudaError_t residency(const Residency** out) {
   constexpr int kMaxDev = 64;
-  static std::atomic<int> cache[kMaxDev][kClusterMax + 1][kGradCtas + 1];
+  static Residency table[kMaxDev];
+  static std::once_flag once[kMaxDev];
+  static cudaError_t err[kMaxDev];
   int dev = 0;
-  cudaGetDevice(&dev);
-  const bool slot = dev >= 0 && dev < kMaxDev;
-  if (slot && cache[dev][c][k].load(std::memory_order_relaxed) > 0) return cache[dev][c][k].load(std::memory_order_relaxed);
-  int n = 0;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(c);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(c * 1024));
-  cfg.blockDim = dim3(kGradThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(grad_smem(k));
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const GradKernel f = grad_kernel(true, k);
-  if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, grad_smem(k)) != cudaSuccess ||
-      cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, f, &cfg) != cudaSuccess) {
-    cudaGetLastError();
-    return std::max(1, device_sm_count() * k / c);    // sizes can be asked without a device
-  }
-  if (slot && n > 0) cache[dev][c][k].store(n, std::memory_order_relaxed);
-  return n;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  std::call_once(once[dev], [&] {
+    Residency& t = table[dev];
+    t.sms = device_sm_count();
+    cudaError_t& r = err[dev];
+    for (int k = 1; k <= kGradCtas && r == cudaSuccess; ++k) {
+      for (const bool vec : {false, true}) for (const bool is_long : {false, true}) {
+        const GradKernel f = grad_kernel(vec, is_long, k);
+        if (f == nullptr) continue;
+        if (r == cudaSuccess) r = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, grad_smem(k));
+        if (r == cudaSuccess) r = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      }
+      for (const int c : kClusterSizes) {
+        cudaLaunchConfig_t cfg{};
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = static_cast<unsigned>(c);
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(c * 1024));
+        cfg.blockDim = dim3(kGradThreads);
+        cfg.dynamicSmemBytes = static_cast<size_t>(grad_smem(k));
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if (r == cudaSuccess) r = cudaOccupancyMaxActiveClusters(&t.clusters[k][c], grad_kernel(true, false, k), &cfg);
+      }
+    }
+  });
+  *out = &table[dev];
+  return err[dev];
 }
 
 // Slices of the tokens, as `clusters` clusters of `cluster` CTAs, k CTAs an SM: the counts with the
@@ -458,28 +502,32 @@ struct GradPlan {
 };
 GradPlan grad_plan(int64_t M, int64_t K, int r) {
   const int64_t groups = (K + kGradCols - 1) / kGradCols * ((r + kGradRanks - 1) / kGradRanks);
-  const int64_t steps = (M + 15) / 16, sms = device_sm_count();
+  const int64_t steps = std::max<int64_t>((M + 15) / 16, 1);
+  const Residency* res = nullptr;
+  if (residency(&res) != cudaSuccess) {    // sizes can be asked without a device
+    cudaGetLastError();
+    return GradPlan{1, 1, 1, steps};
+  }
   constexpr int kStepNs[kGradCtas + 1] = {0, 420, 580, 820};
   GradPlan best{1, 1, 1, steps};
   int64_t best_ns = INT64_MAX;
-  for (int n = 1; n <= 8; ++n)
-    for (int c = 1; c <= kClusterMax && n * c <= std::max<int64_t>(steps, 1); ++c) {
+  for (int64_t n = 1; n <= 8; n *= 2)
+    for (const int c : kClusterSizes) {
+      if (n * c > steps) continue;
       const int64_t per = (steps + n * c - 1) / (n * c);
-      const int k = static_cast<int>(std::min<int64_t>(kGradCtas, (groups * n * c + sms - 1) / sms));
-      const int fit = resident_clusters(c, k);
+      int k = static_cast<int>(std::min<int64_t>(kGradCtas, (groups * n * c + res->sms - 1) / res->sms));
+      if (per > kSliceSteps) k = std::min(k, 2);    // (their second sums take a third CTA's registers)
+      const int fit = res->clusters[k][c];
       if (fit < 1) continue;
       const int64_t waves = (groups * n + fit - 1) / fit;
       const int64_t ns = waves * (per * kStepNs[k] + 3000) + (c > 1 ? 1000 : 0) + (n > 1 ? 4000 + 100 * n : 0);
-      if (ns < best_ns) best = GradPlan{c, n, k, per}, best_ns = ns;
+      if (ns < best_ns) best = GradPlan{c, static_cast<int>(n), k, per}, best_ns = ns;
     }
   return best;
 }
 
 cudaError_t launch_grad(const ActGradArgs& a, const GradPlan& g, float* part, cudaStream_t st) {
-  const GradKernel f = grad_kernel(a.K % 16 == 0, g.k);
-  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, grad_smem(g.k));
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
+  const GradKernel f = grad_kernel(a.K % 16 == 0, g.per > kSliceSteps, g.k);
   note_launch();
   const dim3 grid(static_cast<unsigned>(g.cluster * g.clusters), static_cast<unsigned>((a.K + kGradCols - 1) / kGradCols),
                   static_cast<unsigned>((a.r + kGradRanks - 1) / kGradRanks));

@@ -149,6 +149,20 @@ def test_grad_a_ranges(lib, gmag, smag):
     _within(dA, ot.grad_a(G, x, 1.0), _grad_bound(G, x, 1.0, M) + 2.0 ** -140, "dA")
 
 
+@pytest.mark.parametrize("M,K,r", [(8192, 14336, 64), (30000, 1024, 16), (5000, 777, 20)])
+def test_grad_a_of_long_batches(lib, M, K, r):
+    """More tokens than a slice adds up in the tensor cores: the same bound, in norm 1e-5 (float32)."""
+    gen = torch.Generator(device=DEV).manual_seed(M)
+    c = b.qlora_act8_quantize(torch.randn(M, K, generator=gen, device=DEV))
+    G = torch.randn(M, r, generator=gen, device=DEV) * 1e-3
+    dA = b.qlora_act8_grad_a(G, c, float(r)).double()
+    x = c.codes.double() * c.scales.double().repeat_interleave(128, 1)[:, :K]
+    want, mag = G.double().T @ x, G.double().abs().T @ x.abs()
+    assert ((dA - want).abs() <= (2.0 ** -21 + (M + 64) * U) * mag).all()
+    assert (dA - want).norm() <= 1e-5 * want.norm()
+    _ok()
+
+
 def test_grad_a_no_tokens_and_nan(lib):
     c = b.Act8.empty(0, 256)
     assert not b.qlora_act8_grad_a(torch.empty(0, 4, device=DEV), c, 1.0).any()
