@@ -807,7 +807,8 @@ int64_t piece_cols(int64_t M, int64_t V, int64_t D, bool stored, bool grad) {
   return ((V + pieces - 1) / pieces + kTile - 1) / kTile * kTile;
 }
 
-int max_clusters() { return device_sm_count() / kCluster; }
+// (at least one: sizes can be asked without a device)
+int max_clusters() { return std::max(1, device_sm_count() / kCluster); }
 
 // Parts of the gradient's contraction: enough that the tiles fill the SMs, each part at least
 // four steps long; of those up to 32 the one with the least rounds of steps (and 6 steps for a
