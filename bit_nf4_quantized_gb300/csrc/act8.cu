@@ -34,7 +34,7 @@ struct ChunkWalk {
 // Four lanes to a block of 128, 32 values each (train_ops.cuh): with 8 values a lane the block's
 // reduction and divisions took longer than its bytes (4096 x 14336 bf16: 51 us; with 32, 29 us,
 // 0.91 of the measured copy bandwidth).  Rows that are not 16-byte aligned keep 8 values a lane,
-// whose narrow accesses then share sectors (4096 x 4095: 27 us; with 32 a lane, 45).  Bound by
+// whose narrow accesses then share sectors (4096 x 4095: 18.5 us; with 32 a lane, 45 in single elements).  Bound by
 // HBM: the activation once, one byte a value and 4 / 128 out.
 template <bool kVec>
 constexpr int quant_chunks() { return kVec ? 4 : 1; }
@@ -45,15 +45,16 @@ __global__ void __launch_bounds__(kThreads) act8_quantize(const T* x, int64_t M,
   pdl_wait();
   const int64_t L = (K + kActBlock - 1) / kActBlock * (kActLanes / kN);   // lanes of a row
   const ChunkWalk w(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, L);
+  const int p = kVec ? 0 : row_parity(w.m, K);
   float v[kN][8];
 #pragma unroll
   for (int u = 0; u < kN; ++u) {
-    if (w.m < M) load8<T, kVec>(x + w.m * K, chunk_of(w.c, kN, u), K, v[u]);
+    if (w.m < M) load8<T, kVec>(x + w.m * K, chunk_of(w.c, kN, u), K, v[u], p);
     else
       for (int j = 0; j < 8; ++j) v[u][j] = 0.0f;
   }
   const Quantized<kN> q = quantize_block<kN>(v);
-  if (w.m < M) store_block<kVec, kN>(out, w.m, w.c, K, q, status);
+  if (w.m < M) store_block<kVec, kN>(out, w.m, w.c, K, q, status, p);
 }
 
 template <typename T, bool kVec>
@@ -67,22 +68,23 @@ __global__ void __launch_bounds__(kThreads) act8_dequantize(Act8View in, int64_t
 #pragma unroll
   for (int u = 0; u < kPer; ++u, at.next(C)) {
     const int64_t m = min(at.m, M - 1);
-    q[u] = load_codes<kVec>(in.codes + m * K, at.c, K);
+    q[u] = load_codes<kVec>(in.codes + m * K, at.c, K, kVec ? 0 : row_parity(m, K));
     sc[u] = in.scales[m * nb + at.c / kActLanes];
   }
 #pragma unroll
   for (int u = 0; u < kPer; ++u, w.next(C)) {
     if (w.m >= M) continue;
+    const int p = kVec ? 0 : row_parity(w.m, K);
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = code_value(q[u], j) * sc[u];
     if (weight != nullptr) {
       float g[8];
-      load8<float, kVec>(weight, w.c, K, g);
+      load_vector8<kVec>(weight, w.c, K, g, p);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= g[j];
     }
-    store8<T, kVec>(out + w.m * K, w.c, K, v);
+    store8<T, kVec>(out + w.m * K, w.c, K, v, p);
   }
 }
 

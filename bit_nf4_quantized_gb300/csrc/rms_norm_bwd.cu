@@ -6,10 +6,15 @@
 // One pass: a row's dn and n live in the registers of a group of threads between the sum and
 // the store.  Groups walk over rows with a fixed set of columns for each thread, so dweight's
 // sums stay in registers too; each group writes them once and norm_dweight adds the groups in
-// a fixed order.  Rows of whole 16-byte pieces come through a ring of bulk copies (row_ring.cuh);
-// others, and rows too long for the ring, are loaded by the threads themselves.  Bound by HBM: dy, dresidual, dx and h (or one byte a value) once each.
+// a fixed order.  Rows come through a ring of bulk copies (row_ring.cuh); short ones (ring_chunks) and
+// those too long for it are loaded by the threads themselves.  Bound by HBM: dy, dresidual, dx and
+// h (or one byte a value) once each: 4096 x 4096 bf16, 134 MB, 24 us, 0.82 of the measured copy
+// bandwidth (loaded by the threads: 38 us); with dweight 32 us.  Rows that are not 16-byte aligned are
+// bound by their instructions, in pairs rather than eights: 4096 x 4095, 37 us from h, 29 us from the
+// checkpoint, with dweight 42 and 33 (by single elements, loaded by the threads: 48 us).
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "row_ring.cuh"
 
@@ -30,11 +35,13 @@ __global__ void __launch_bounds__(512) rms_norm_bwd(const NormBwdArgs a) {
   const int64_t nb = (a.K + kActBlock - 1) / kActBlock;
   const float invK = 1.0f / static_cast<float>(a.K);
   float* part = kDw ? a.partial + (static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y) * a.K : nullptr;
+  // a group's rows all start at the same parity (bwd_shape), so its threads' columns are the same for all
+  const int p = kVec ? 0 : row_parity(static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y, a.K);
   constexpr bool kHoldW = kNv == 1 || kNv == 2;   // longer rows read the weight again (from L1)
   float dw[kN][8], w[kN][8];
 #pragma unroll
   for (int i = 0; i < kN; ++i) {
-    if (kHoldW) load8<float, kVec>(a.weight, threadIdx.x + static_cast<int64_t>(i) * blockDim.x, a.K, w[i]);
+    if (kHoldW) load_vector8<kVec>(a.weight, threadIdx.x + static_cast<int64_t>(i) * blockDim.x, a.K, w[i], p);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   }
@@ -46,11 +53,11 @@ __global__ void __launch_bounds__(512) rms_norm_bwd(const NormBwdArgs a) {
     const float rstd = on ? a.rstd[m] : 0.0f;
     auto load_n = [&](int64_t c, float (&n)[8]) {
       if (a.h != nullptr) {
-        load8<T, kVec>(static_cast<const T*>(a.h) + at, c, a.K, n);
+        load8<T, kVec>(static_cast<const T*>(a.h) + at, c, a.K, n, p);
 #pragma unroll
         for (int j = 0; j < 8; ++j) n[j] *= rstd;
       } else {
-        const uint2 q = load_codes<kVec>(a.act.codes + at, c, a.K);
+        const uint2 q = load_codes<kVec>(a.act.codes + at, c, a.K, p);
         const float sc = (c / kActLanes) * kActBlock < a.K ? a.act.scales[(on ? m : 0) * nb + c / kActLanes] : 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) n[j] = code_value(q, j) * sc;
@@ -58,13 +65,13 @@ __global__ void __launch_bounds__(512) rms_norm_bwd(const NormBwdArgs a) {
     };
     auto finish = [&](int64_t c, const float (&g)[8], const float (&n)[8], float mean) {
       float o[8];
-      if (a.dresidual != nullptr) load8<T, kVec>(static_cast<const T*>(a.dresidual) + at, c, a.K, o);
+      if (a.dresidual != nullptr) load8<T, kVec>(static_cast<const T*>(a.dresidual) + at, c, a.K, o, p);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float d = rstd * (g[j] - n[j] * mean);
         o[j] = a.dresidual != nullptr ? d + o[j] : d;
       }
-      store8<T, kVec>(static_cast<T*>(a.dx) + at, c, a.K, o);
+      store8<T, kVec>(static_cast<T*>(a.dx) + at, c, a.K, o, p);
     };
     float s = 0.0f;
     if (kNv > 0) {
@@ -73,9 +80,9 @@ __global__ void __launch_bounds__(512) rms_norm_bwd(const NormBwdArgs a) {
       for (int i = 0; i < kN; ++i) {
         const int64_t c = threadIdx.x + static_cast<int64_t>(i) * blockDim.x;
         if (on) {
-          load8<T, kVec>(static_cast<const T*>(a.dy) + at, c, a.K, g[i]);
+          load8<T, kVec>(static_cast<const T*>(a.dy) + at, c, a.K, g[i], p);
           load_n(c, n[i]);
-          if (!kHoldW) load8<float, kVec>(a.weight, c, a.K, w[0]);
+          if (!kHoldW) load_vector8<kVec>(a.weight, c, a.K, w[0], p);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             if (kDw) dw[i][j] = fmaf(g[i][j], n[i][j], dw[i][j]);
@@ -92,20 +99,20 @@ __global__ void __launch_bounds__(512) rms_norm_bwd(const NormBwdArgs a) {
     } else {
       float g[8], n[8];
       auto load_g = [&](int64_t c) {
-        load8<T, kVec>(static_cast<const T*>(a.dy) + at, c, a.K, g);
+        load8<T, kVec>(static_cast<const T*>(a.dy) + at, c, a.K, g, p);
         load_n(c, n);
       };
       if (on) {
         for (int64_t c = threadIdx.x; c < C; c += blockDim.x) {
           float wc[8];
           load_g(c);
-          load8<float, kVec>(a.weight, c, a.K, wc);
+          load_vector8<kVec>(a.weight, c, a.K, wc, p);
           if (kDw) {
-            float p[8];
-            if (it > 0) load8<float, kVec>(part, c, a.K, p);
+            float d[8];
+            if (it > 0) load8<float, kVec>(part, c, a.K, d, p);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) p[j] = fmaf(g[j], n[j], it > 0 ? p[j] : 0.0f);
-            store8<float, kVec>(part, c, a.K, p);
+            for (int j = 0; j < 8; ++j) d[j] = fmaf(g[j], n[j], it > 0 ? d[j] : 0.0f);
+            store8<float, kVec>(part, c, a.K, d, p);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) s = fmaf(g[j] * wc[j], n[j], s);
@@ -116,7 +123,7 @@ __global__ void __launch_bounds__(512) rms_norm_bwd(const NormBwdArgs a) {
         for (int64_t c = threadIdx.x; c < C; c += blockDim.x) {
           float wc[8];
           load_g(c);
-          load8<float, kVec>(a.weight, c, a.K, wc);
+          load_vector8<kVec>(a.weight, c, a.K, wc, p);
 #pragma unroll
           for (int j = 0; j < 8; ++j) g[j] *= wc[j];
           finish(c, g, n, mean);
@@ -127,13 +134,13 @@ __global__ void __launch_bounds__(512) rms_norm_bwd(const NormBwdArgs a) {
   if (kDw && kNv > 0) {
 #pragma unroll
     for (int i = 0; i < kN; ++i)
-      store8<float, kVec>(part, threadIdx.x + static_cast<int64_t>(i) * blockDim.x, a.K, dw[i]);
+      store8<float, kVec>(part, threadIdx.x + static_cast<int64_t>(i) * blockDim.x, a.K, dw[i], p);
   }
 }
 
 // Workers walk over rows: G threads a worker, blockDim.x / G workers a CTA.  kCk: n comes from the
-// checkpoint (K % 16 == 0: whole 16-byte pieces of codes), else from h.
-template <typename T, int kN, bool kCk, bool kDw>
+// checkpoint, else from h.
+template <typename T, bool kVec, int kN, bool kCk, bool kDw>
 __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, int G, int stages, int* status) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[2 * 32];
@@ -142,7 +149,8 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, in
   const int w = threadIdx.x / G, t = threadIdx.x - w * G;
   const uint32_t row_bytes = static_cast<uint32_t>(a.K * sizeof(T));
   const uint32_t saved_bytes = kCk ? static_cast<uint32_t>(a.K) : row_bytes;
-  const uint32_t bytes = row_bytes * (a.dresidual != nullptr ? 2 : 1) + saved_bytes;
+  const uint32_t slot = row_slot<kVec>(row_bytes), saved_slot = kCk ? row_slot<false>(saved_bytes) : slot;
+  const uint32_t bytes = slot * (a.dresidual != nullptr ? 2 : 1) + saved_slot;
   uint8_t* ring = smem + static_cast<size_t>(w) * stages * bytes;
   const uint32_t ring_at = tc::smem_u32(ring), bar_at = tc::smem_u32(bars + w * kRingStagesMax);
   if (t == 0)
@@ -155,74 +163,96 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, in
   const int64_t workers = static_cast<int64_t>(gridDim.x) * (blockDim.x / G);
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (blockDim.x / G) + w;
   const int64_t nb = (a.K + kActBlock - 1) / kActBlock;
-  const int64_t blk = min(static_cast<int64_t>(t / (kActLanes / kN)), nb - 1);
+  constexpr int kScales = kVec ? 1 : kN;             // blocks that a thread's chunks belong to
+  auto block = [&](int u) { return min(static_cast<int64_t>(ring_chunk<kVec, kN>(t, G, u) / kActLanes), nb - 1); };
   const float invK = 1.0f / static_cast<float>(a.K);
+  const int p = kVec ? 0 : row_parity(first, a.K);
   auto issue = [&](int64_t m, int s) {
     if (m >= a.M) return;
     const uint32_t dst = ring_at + s * bytes, bar = bar_at + 8 * s;
-    tc::mbar_expect_tx(bar, bytes);
-    bulk_copy(dst, static_cast<const T*>(a.dy) + m * a.K, row_bytes, bar);
-    if (kCk) bulk_copy(dst + row_bytes, a.act.codes + m * a.K, saved_bytes, bar);
-    else bulk_copy(dst + row_bytes, static_cast<const T*>(a.h) + m * a.K, saved_bytes, bar);
-    if (a.dresidual != nullptr)
-      bulk_copy(dst + row_bytes + saved_bytes, static_cast<const T*>(a.dresidual) + m * a.K, row_bytes, bar);
+    uint8_t* at = ring + s * bytes;
+    const RowCopy<kVec> dy(a.dy, m, a.M, row_bytes, dst, at);
+    const RowCopy<kVec && !kCk> saved(kCk ? static_cast<const void*>(a.act.codes) : a.h, m, a.M, saved_bytes, dst + slot, at + slot);
+    if (a.dresidual != nullptr) {
+      const RowCopy<kVec> dres(a.dresidual, m, a.M, row_bytes, dst + slot + saved_slot, at + slot + saved_slot);
+      tc::mbar_expect_tx(bar, dy.bytes + saved.bytes + dres.bytes);
+      dres.issue(bar);
+    } else {
+      tc::mbar_expect_tx(bar, dy.bytes + saved.bytes);
+    }
+    dy.issue(bar);
+    saved.issue(bar);
   };
   if (t == 0)
     for (int s = 0; s < stages; ++s) issue(first + s * workers, s);
-  float dw[kN][8];
+  // the weight in registers where there is room and reading it again would not be two wide loads
+  constexpr bool kHoldW = !kVec && kN == 2;
+  float dw[kN][8], held[kHoldW ? kN : 1][8];
 #pragma unroll
-  for (int u = 0; u < kN; ++u)
+  for (int u = 0; u < kN; ++u) {
+    if (kHoldW) load_vector8<kVec, int64_t>(a.weight, ring_chunk<kVec, kN>(t, G, u), a.K, held[kHoldW ? u : 0], p);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[u][j] = 0.0f;
-  // the row's rstd and the block's scale, one row ahead
+  }
+  // the row's rstd and the blocks' scales, one row ahead
   float rstd_next = first < a.M ? a.rstd[first] : 0.0f;
-  float scale_next = kCk && first < a.M ? a.act.scales[first * nb + blk] : 0.0f;
+  float scale_next[kScales];
+#pragma unroll
+  for (int u = 0; u < kScales; ++u) scale_next[u] = kCk && first < a.M ? a.act.scales[first * nb + block(u)] : 0.0f;
   int s = 0, turn = 0;
   uint32_t ph = 0;
   for (int64_t m = first; m < a.M; m += workers, turn ^= 1) {
-    const float rstd = rstd_next, scale = scale_next;
+    const std::conditional_t<kVec, int64_t, int> K = kVec ? a.K : not_kept(a.K);
+    const float rstd = rstd_next;
+    float scale[kScales];
+#pragma unroll
+    for (int u = 0; u < kScales; ++u) scale[u] = scale_next[u];
     if (m + workers < a.M) {
       rstd_next = a.rstd[m + workers];
-      if (kCk) scale_next = a.act.scales[(m + workers) * nb + blk];
+#pragma unroll
+      for (int u = 0; u < kScales; ++u)
+        if (kCk) scale_next[u] = a.act.scales[(m + workers) * nb + block(u)];
     }
     tc::mbar_wait(bar_at + 8 * s, ph, &gave_up, status);   // see rms_norm_fwd_ring
-    const uint8_t* stage = ring + s * bytes;
+    const uint32_t shift = kVec ? 0 : row_shift(m, row_bytes);
+    const uint8_t* stage = ring + s * bytes + shift;
+    const uint8_t* saved = ring + s * bytes + slot + (kCk ? row_shift(m, saved_bytes) : shift);
     float g[kN][8], n[kN][8];
     float sum = 0.0f;
 #pragma unroll
     for (int u = 0; u < kN; ++u) {
-      const int64_t c = chunk_of(t, kN, u);
+      const auto c = ring_chunk<kVec, kN>(t, G, u);
       float wt[8];
-      load8<float, true>(a.weight, c, a.K, wt);
-      ring8<T>(stage, c, a.K, g[u]);
+      if (!kHoldW) load_vector8<kVec>(a.weight, c, K, wt, p);
+      ring8<T, kVec>(stage, c, K, g[u], p);
       if (kCk) {
-        const uint2 q = load_codes<true>(reinterpret_cast<const int8_t*>(stage + row_bytes), c, a.K);
+        const uint2 q = ring_codes<kVec>(saved, c, K, p);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) n[u][j] = code_value(q, j) * scale;
+        for (int j = 0; j < 8; ++j) n[u][j] = code_value(q, j) * scale[kVec ? 0 : u];
       } else {
-        ring8<T>(stage + row_bytes, c, a.K, n[u]);
+        ring8<T, kVec>(saved, c, K, n[u], p);
 #pragma unroll
         for (int j = 0; j < 8; ++j) n[u][j] *= rstd;
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (kDw) dw[u][j] = fmaf(g[u][j], n[u][j], dw[u][j]);
-        g[u][j] *= wt[j];
+        g[u][j] *= kHoldW ? held[kHoldW ? u : 0][j] : wt[j];
         sum = fmaf(g[u][j], n[u][j], sum);
       }
     }
     const float mean = worker_sum(sum, G, red, turn) * invK;
 #pragma unroll
     for (int u = 0; u < kN; ++u) {
-      const int64_t c = chunk_of(t, kN, u);
+      const auto c = ring_chunk<kVec, kN>(t, G, u);
       float o[8];
-      if (a.dresidual != nullptr) ring8<T>(stage + row_bytes + saved_bytes, c, a.K, o);
+      if (a.dresidual != nullptr) ring8<T, kVec>(stage + slot + saved_slot, c, K, o, p);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float d = rstd * (g[u][j] - n[u][j] * mean);
         o[j] = a.dresidual != nullptr ? d + o[j] : d;
       }
-      store8<T, true>(static_cast<T*>(a.dx) + m * a.K, c, a.K, o);
+      store8<T, kVec>(static_cast<T*>(a.dx) + m * a.K, c, K, o, p);
     }
     if (G == 32) __syncwarp();
     else __syncthreads();
@@ -237,7 +267,7 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, in
   if (kDw) {
     float* part = a.partial + first * a.K;
 #pragma unroll
-    for (int u = 0; u < kN; ++u) store8<float, true>(part, chunk_of(t, kN, u), a.K, dw[u]);
+    for (int u = 0; u < kN; ++u) store8<float, kVec, int64_t>(part, ring_chunk<kVec, kN>(t, G, u), a.K, dw[u], p);
   }
 }
 
@@ -271,8 +301,9 @@ BwdShape bwd_shape(int64_t M, int64_t K) {
   BwdShape b;
   b.nv = C <= 512 ? 1 : C <= 1024 ? 2 : C <= 2048 ? 4 : 0;
   b.row = b.nv > 0 ? row_shape(C, b.nv) : RowShape{512, 1};
-  // about 1024 threads an SM, each walking over rows
-  const int64_t ctas = static_cast<int64_t>(device_sm_count()) * std::max(1, 1024 / (b.row.G * b.row.R));
+  // about 1024 threads an SM, each walking over rows an even number apart, so that a group's rows
+  // start at the same parity (row_parity)
+  const int64_t ctas = (static_cast<int64_t>(device_sm_count()) * std::max(1, 1024 / (b.row.G * b.row.R)) + 1) / 2 * 2;
   b.grid = static_cast<int>(std::min(ctas, (M + b.row.R - 1) / b.row.R));
   return b;
 }
@@ -281,26 +312,32 @@ BwdShape bwd_shape(int64_t M, int64_t K) {
 // sums beside a row's dn and n, four are more than its registers (4096 x 4096: 42 us with four, 32 with
 // two); short rows have so many workers that adding up their sums costs more than the ring gains
 // (4096 x 576: 14 us, loaded by the threads 11; 4096 x 2048: 20 and 22).
-int ring_chunks(int64_t K, bool dw) { return !dw ? 4 : K <= 1024 ? 0 : K <= 8192 ? 2 : 4; }
+int ring_chunks(int64_t K, bool dw) {
+  const bool vec = K % 8 == 0;
+  if (vec && !dw) return 4;
+  return vec && K <= 1024 ? 0 : K <= kRingFewK ? 2 : 4;
+}
 
 // The ring's shape for a call, from what a row's inputs take (an element of `elem` bytes).
 RingShape bwd_ring(int64_t M, int64_t K, size_t elem, bool ck, bool dres, int n) {
-  if (n == 0 || K % (ck ? 16 : 8) != 0) return RingShape{};
-  return ring_shape(M, K, K * elem * (dres ? 2 : 1) + K * (ck ? 1 : elem), n == 4 ? 128 : 104, n);
+  if (n == 0 || K > kRingMaxK) return RingShape{};
+  const uint32_t row = static_cast<uint32_t>(K * elem), slot = K % 8 == 0 ? row_slot<true>(row) : row_slot<false>(row);
+  return ring_shape(M, K, slot * (dres ? 2 : 1) + (ck ? row_slot<false>(static_cast<uint32_t>(K)) : slot),
+                    n == 4 || K % 8 != 0 ? 128 : 104, n);
 }
 
-template <typename T, int kN, bool kCk, bool kDw>
+template <typename T, bool kVec, int kN, bool kCk, bool kDw>
 cudaError_t launch_ring(const NormBwdArgs& a, const RingShape& r, int* status, cudaStream_t st) {
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
   std::call_once(once, [&] {
-    err = cudaFuncSetAttribute(rms_norm_bwd_ring<T, kN, kCk, kDw>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(kRingSmemMax));
+    err = cudaFuncSetAttribute(rms_norm_bwd_ring<T, kVec, kN, kCk, kDw>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(kRingSmemMax + kRingPad));
   });
   if (err != cudaSuccess) return err;
   note_launch();
-  return launch_pdl(rms_norm_bwd_ring<T, kN, kCk, kDw>, dim3(r.grid), dim3(r.G * r.workers), r.smem, st, 1, a, r.G, r.stages,
-                    status);
+  return launch_pdl(rms_norm_bwd_ring<T, kVec, kN, kCk, kDw>, dim3(r.grid), dim3(r.G * r.workers), r.smem, st, 1, a, r.G,
+                    r.stages, status);
 }
 
 cudaError_t add_groups(const NormBwdArgs& a, int64_t groups, cudaStream_t st) {
@@ -311,18 +348,17 @@ cudaError_t add_groups(const NormBwdArgs& a, int64_t groups, cudaStream_t st) {
 
 template <typename T, bool kVec, bool kDw>
 cudaError_t launch(const NormBwdArgs& a, int* status, cudaStream_t st) {
-  if (kVec) {
-    const bool ck = a.h == nullptr;
-    const int n = ring_chunks(a.K, kDw);
-    const RingShape r = bwd_ring(a.M, a.K, sizeof(T), ck, a.dresidual != nullptr, n);
-    if (r.stages > 0) {
-      constexpr int kFew = kDw ? 2 : 4;
-      const cudaError_t e = n == 4 ? (ck ? launch_ring<T, 4, true, kDw>(a, r, status, st) : launch_ring<T, 4, false, kDw>(a, r, status, st))
-                                   : (ck ? launch_ring<T, kFew, true, kDw>(a, r, status, st)
-                                         : launch_ring<T, kFew, false, kDw>(a, r, status, st));
-      if (e != cudaSuccess || !kDw) return e;
-      return add_groups(a, std::min<int64_t>(static_cast<int64_t>(r.grid) * r.workers, a.M), st);
-    }
+  const bool ck = a.h == nullptr;
+  const int n = ring_chunks(a.K, kDw);
+  const RingShape r = bwd_ring(a.M, a.K, sizeof(T), ck, a.dresidual != nullptr, n);
+  if (r.stages > 0) {
+    constexpr int kFew = kVec && !kDw ? 4 : 2;
+    const cudaError_t e =
+        n == 4 ? (ck ? launch_ring<T, kVec, 4, true, kDw>(a, r, status, st) : launch_ring<T, kVec, 4, false, kDw>(a, r, status, st))
+               : (ck ? launch_ring<T, kVec, kFew, true, kDw>(a, r, status, st)
+                     : launch_ring<T, kVec, kFew, false, kDw>(a, r, status, st));
+    if (e != cudaSuccess || !kDw) return e;
+    return add_groups(a, std::min<int64_t>(static_cast<int64_t>(r.grid) * r.workers, a.M), st);
   }
   const BwdShape b = bwd_shape(a.M, a.K);
   const dim3 grid(static_cast<unsigned>(b.grid)), block(b.row.G, b.row.R);

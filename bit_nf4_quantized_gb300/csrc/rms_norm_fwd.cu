@@ -5,15 +5,24 @@
 // One pass: a row lives in the registers of a group of threads from its load to the stores of
 // h, y and n's codes.  Bound by HBM: x, residual, h and y once each, one byte a value and
 // 4 / 128 for the checkpoint.  h is rounded when it is stored; the norm is taken of the fp32
-// sum.  Rows of whole 16-byte pieces come through a ring of bulk copies (row_ring.cuh); others,
-// and rows too long for the ring, are loaded by the threads themselves.
+// sum.  Rows come through a ring of bulk copies (row_ring.cuh); those too long for it, and short
+// ones that are not 16-byte aligned, are loaded by the threads themselves.  4096 x 4096 bf16 with
+// residual and checkpoint, 152 MB: 26 us, 0.86 of the measured copy bandwidth (loaded by the
+// threads: 37 us).  4096 x 4095, bound by its instructions: 42 us (by single elements: 61 us).
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "row_ring.cuh"
 
 namespace qnf4 {
 namespace {
+
+// A thread's registers with two chunks in pairs: three CTAs of 256 threads an SM.
+constexpr int kPairRegs = 80;
+// Rows of pairs up to this length are loaded by their threads (4096 x 577: 10 us, by the ring 12;
+// 777 x 1531: 6.3 both; 4096 x 4095: 49 and 42).
+constexpr int64_t kPairDirectK = 1024;
 
 // kNv = 0: rows longer than the registers of a CTA hold; the row is read twice.
 template <typename T, bool kVec, int kNv>
@@ -25,13 +34,14 @@ __global__ void __launch_bounds__(512) rms_norm_fwd(const NormFwdArgs a, int* st
   const bool on = m < a.M;
   const int64_t C = (a.K + kActBlock - 1) / kActBlock * kActLanes;   // whole blocks of lanes
   const int64_t at = m * a.K;
+  const int p = kVec ? 0 : row_parity(m, a.K);
   const T* x = static_cast<const T*>(a.x) + at;
   const T* res = static_cast<const T*>(a.residual) + (a.residual != nullptr ? at : 0);
   auto load = [&](int64_t c, float (&v)[8]) {
-    load8<T, kVec>(x, c, a.K, v);
+    load8<T, kVec>(x, c, a.K, v, p);
     if (a.residual != nullptr) {
       float r[8];
-      load8<T, kVec>(res, c, a.K, r);
+      load8<T, kVec>(res, c, a.K, r, p);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += r[j];
     }
@@ -42,16 +52,16 @@ __global__ void __launch_bounds__(512) rms_norm_fwd(const NormFwdArgs a, int* st
 #pragma unroll
     for (int u = 0; u < kN; ++u) {
       const int64_t c = chunk_of(t, kN, u);
-      if (on && a.h != nullptr) store8<T, kVec>(static_cast<T*>(a.h) + at, c, a.K, h[u]);
+      if (on && a.h != nullptr) store8<T, kVec>(static_cast<T*>(a.h) + at, c, a.K, h[u], p);
       float y[8], w[8];
-      load8<float, kVec>(a.weight, c, a.K, w);
+      load_vector8<kVec>(a.weight, c, a.K, w, p);
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[u][j] *= rstd, y[j] = h[u][j] * w[j];
-      if (on) store8<T, kVec>(static_cast<T*>(a.y) + at, c, a.K, y);
+      if (on) store8<T, kVec>(static_cast<T*>(a.y) + at, c, a.K, y, p);
     }
     if (a.act.codes != nullptr) {
       const Quantized<kN> q = quantize_block<kN>(h);
-      if (on) store_block<kVec, kN>(a.act, m, t, a.K, q, status);
+      if (on) store_block<kVec, kN>(a.act, m, t, a.K, q, status, p);
     }
   };
   float ss = 0.0f;
@@ -89,15 +99,15 @@ __global__ void __launch_bounds__(512) rms_norm_fwd(const NormFwdArgs a, int* st
 }
 
 // Workers walk over rows: G threads a worker, blockDim.x / G workers a CTA.
-template <typename T>
-__global__ void __launch_bounds__(512) rms_norm_fwd_ring(const NormFwdArgs a, int G, int stages, int* status) {
+template <typename T, bool kVec, int kN>
+__global__ void __maxnreg__(kN == 2 ? kPairRegs : 128) rms_norm_fwd_ring(const NormFwdArgs a, int G, int stages, int* status) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[2 * 32];
   __shared__ uint64_t bars[kRingWarpWorkers * kRingStagesMax];
   __shared__ int gave_up;
   const int w = threadIdx.x / G, t = threadIdx.x - w * G;
   const uint32_t row_bytes = static_cast<uint32_t>(a.K * sizeof(T));
-  const uint32_t bytes = row_bytes * (a.residual != nullptr ? 2 : 1);
+  const uint32_t slot = row_slot<kVec>(row_bytes), bytes = slot * (a.residual != nullptr ? 2 : 1);
   uint8_t* ring = smem + static_cast<size_t>(w) * stages * bytes;
   const uint32_t ring_at = tc::smem_u32(ring), bar_at = tc::smem_u32(bars + w * kRingStagesMax);
   if (t == 0)
@@ -109,33 +119,42 @@ __global__ void __launch_bounds__(512) rms_norm_fwd_ring(const NormFwdArgs a, in
   pdl_wait();
   const int64_t workers = static_cast<int64_t>(gridDim.x) * (blockDim.x / G);
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (blockDim.x / G) + w;
+  const int p = kVec ? 0 : row_parity(first, a.K);
   auto issue = [&](int64_t m, int s) {
     if (m >= a.M) return;
-    tc::mbar_expect_tx(bar_at + 8 * s, bytes);
-    bulk_copy(ring_at + s * bytes, static_cast<const T*>(a.x) + m * a.K, row_bytes, bar_at + 8 * s);
-    if (a.residual != nullptr)
-      bulk_copy(ring_at + s * bytes + row_bytes, static_cast<const T*>(a.residual) + m * a.K, row_bytes, bar_at + 8 * s);
+    const uint32_t bar = bar_at + 8 * s;
+    const RowCopy<kVec> x(a.x, m, a.M, row_bytes, ring_at + s * bytes, ring + s * bytes);
+    if (a.residual != nullptr) {
+      const RowCopy<kVec> r(a.residual, m, a.M, row_bytes, ring_at + s * bytes + slot, ring + s * bytes + slot);
+      tc::mbar_expect_tx(bar, x.bytes + r.bytes);
+      x.issue(bar);
+      r.issue(bar);
+    } else {
+      tc::mbar_expect_tx(bar, x.bytes);
+      x.issue(bar);
+    }
   };
   if (t == 0)
     for (int s = 0; s < stages; ++s) issue(first + s * workers, s);
-  float wt[kRingN][8];      // the thread's columns are the same for every row
+  float wt[kN][8];      // the thread's columns are the same for every row
 #pragma unroll
-  for (int u = 0; u < kRingN; ++u) load8<float, true>(a.weight, chunk_of(t, kRingN, u), a.K, wt[u]);
+  for (int u = 0; u < kN; ++u) load_vector8<kVec, int64_t>(a.weight, ring_chunk<kVec, kN>(t, G, u), a.K, wt[u], p);
   int s = 0, turn = 0;
   uint32_t ph = 0;
   for (int64_t m = first; m < a.M; m += workers, turn ^= 1) {
+    const std::conditional_t<kVec, int64_t, int> K = kVec ? a.K : not_kept(a.K);
     // a wait that gives up leaves the loop's shape as it is: the later ones return at once
     tc::mbar_wait(bar_at + 8 * s, ph, &gave_up, status);
-    const uint8_t* stage = ring + s * bytes;
-    float h[kRingN][8];
+    const uint8_t* stage = ring + s * bytes + (kVec ? 0 : row_shift(m, row_bytes));
+    float h[kN][8];
     float ss = 0.0f;
 #pragma unroll
-    for (int u = 0; u < kRingN; ++u) {
-      const int64_t c = chunk_of(t, kRingN, u);
-      ring8<T>(stage, c, a.K, h[u]);
+    for (int u = 0; u < kN; ++u) {
+      const auto c = ring_chunk<kVec, kN>(t, G, u);
+      ring8<T, kVec>(stage, c, K, h[u], p);
       if (a.residual != nullptr) {
         float r[8];
-        ring8<T>(stage + row_bytes, c, a.K, r);
+        ring8<T, kVec>(stage + slot, c, K, r, p);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[u][j] += r[j];
       }
@@ -148,17 +167,21 @@ __global__ void __launch_bounds__(512) rms_norm_fwd_ring(const NormFwdArgs a, in
     if (t == 0) a.rstd[m] = rstd;
     const int64_t at = m * a.K;
 #pragma unroll
-    for (int u = 0; u < kRingN; ++u) {
-      const int64_t c = chunk_of(t, kRingN, u);
-      if (a.h != nullptr) store8<T, true>(static_cast<T*>(a.h) + at, c, a.K, h[u]);
+    for (int u = 0; u < kN; ++u) {
+      const auto c = ring_chunk<kVec, kN>(t, G, u);
+      if (a.h != nullptr) store8<T, kVec>(static_cast<T*>(a.h) + at, c, K, h[u], p);
       float y[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[u][j] *= rstd, y[j] = h[u][j] * wt[u][j];
-      store8<T, true>(static_cast<T*>(a.y) + at, c, a.K, y);
+      store8<T, kVec>(static_cast<T*>(a.y) + at, c, K, y, p);
     }
     if (a.act.codes != nullptr) {
-      const Quantized<kRingN> q = quantize_block<kRingN>(h);
-      store_block<true, kRingN>(a.act, m, t, a.K, q, status);
+      if constexpr (kVec) {
+        const Quantized<kN> q = quantize_block<kN>(h);
+        store_block<true, kN>(a.act, m, t, K, q, status);
+      } else {
+        store_ring_blocks<kN>(a.act, m, at, t, G, K, p, h, status);
+      }
     }
     if (++s == stages) s = 0, ph ^= 1u;
   }
@@ -169,25 +192,26 @@ __global__ void __launch_bounds__(512) rms_norm_fwd_ring(const NormFwdArgs a, in
     }
 }
 
-template <typename T>
+template <typename T, bool kVec, int kN>
 cudaError_t launch_ring(const NormFwdArgs& a, const RingShape& r, int* status, cudaStream_t st) {
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
   std::call_once(once, [&] {
-    err = cudaFuncSetAttribute(rms_norm_fwd_ring<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(kRingSmemMax));
+    err = cudaFuncSetAttribute(rms_norm_fwd_ring<T, kVec, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(kRingSmemMax + kRingPad));
   });
   if (err != cudaSuccess) return err;
   note_launch();
-  return launch_pdl(rms_norm_fwd_ring<T>, dim3(r.grid), dim3(r.G * r.workers), r.smem, st, 1, a, r.G, r.stages, status);
+  return launch_pdl(rms_norm_fwd_ring<T, kVec, kN>, dim3(r.grid), dim3(r.G * r.workers), r.smem, st, 1, a, r.G, r.stages, status);
 }
 
 template <typename T, bool kVec>
 cudaError_t launch(const NormFwdArgs& a, int* status, cudaStream_t st) {
-  if (kVec) {
-    const RingShape r = ring_shape(a.M, a.K, a.K * sizeof(T) * (a.residual != nullptr ? 2 : 1), 128);
-    if (r.stages > 0) return launch_ring<T>(a, r, status, st);
-  }
+  const size_t bytes = row_slot<kVec>(static_cast<uint32_t>(std::min(a.K, kRingMaxK) * sizeof(T))) * (a.residual != nullptr ? 2 : 1);
+  constexpr int kFew = kVec ? 4 : 2;
+  const int n = a.K > kRingFewK ? 4 : kFew;
+  const RingShape r = ring_shape(a.M, a.K, bytes, n == 2 ? kPairRegs : 128, n);
+  if (r.stages > 0 && (kVec || a.K > kPairDirectK)) return n == 4 ? launch_ring<T, kVec, 4>(a, r, status, st) : launch_ring<T, kVec, kFew>(a, r, status, st);
   const int64_t C = (a.K + kActBlock - 1) / kActBlock * kActLanes;
   const int nv = C <= 512 ? 1 : C <= 1024 ? 2 : C <= 2048 ? 4 : 0;
   const RowShape s = nv > 0 ? row_shape(C, nv) : RowShape{512, 1};

@@ -1,7 +1,11 @@
 // Rows streamed through shared memory for the norm's kernels: a worker (one warp, or a whole CTA)
 // walks over rows, each row's inputs arrive by bulk copies in a ring of stages, and every thread
-// holds four (or two) chunks of one block of the row in registers (train_ops.cuh).  The copies need no
+// holds four (or two) chunks of the row in registers (train_ops.cuh).  The copies need no
 // registers and stay in flight across the reductions, which is what keeps HBM busy.
+//
+// A bulk copy moves whole 16-byte pieces.  Rows that start or end inside one are copied with the
+// pieces around them and read in pairs (train_ops.cuh) from where they start in the stage.  A worker's rows are an
+// even number apart, so they all start at the same parity and a thread's columns are the same for all.
 #pragma once
 
 #include "tc_ptx.cuh"
@@ -10,8 +14,10 @@
 namespace qnf4 {
 
 constexpr int kRingN = 4;                        // chunks a thread holds, where nothing else is said
+constexpr int64_t kRingMaxK = 16384, kRingFewK = 8192;   // the longest rows of 512 threads with four chunks or two
 constexpr int kRingStagesMax = 4;
 constexpr size_t kRingSmemMax = 200 * 1024;      // a CTA's ring at most; two stages must fit
+constexpr size_t kRingPad = 1024;                // behind the last stage: a last block's pairs are read whole
 constexpr int kRingWarpWorkers = 4;              // workers of a CTA where a worker is a warp
 
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -20,14 +26,45 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// A row of `bytes` in a stage: as it is, or with the pieces around its ends.
+template <bool kWhole>
+__host__ __device__ constexpr uint32_t row_slot(uint32_t bytes) { return kWhole ? bytes : (bytes + 15) / 16 * 16 + 16; }
+
+// The copy of row m of a [M] x row_bytes tensor to dst, where it starts row_shift behind; `bytes`: what
+// the barrier will see.  The last row's last piece may end behind the tensor: its bytes are copied here.
+template <bool kWhole>
+struct RowCopy {
+  const uint8_t* src;
+  uint32_t dst, bytes;
+  __device__ __forceinline__ RowCopy(const void* base, int64_t m, int64_t M, uint32_t row_bytes, uint32_t dst_, uint8_t* stage)
+      : dst(dst_), bytes(row_bytes) {
+    const uint8_t* b = static_cast<const uint8_t*>(base);
+    const int64_t at = m * static_cast<int64_t>(row_bytes);
+    src = b + at;
+    if (!kWhole) {
+      const int64_t lo = at & ~int64_t(15), hi = (at + row_bytes + 15) & ~int64_t(15);
+      src = b + lo, bytes = static_cast<uint32_t>(hi - lo);
+      const int64_t end = M * static_cast<int64_t>(row_bytes);
+      if (hi > end) {
+        bytes -= 16;
+        for (uint32_t i = bytes; lo + i < end; ++i) stage[i] = src[i];
+      }
+    }
+  }
+  __device__ __forceinline__ void issue(uint32_t bar) const { bulk_copy(dst, src, bytes, bar); }
+};
+__device__ __forceinline__ uint32_t row_shift(int64_t m, uint32_t row_bytes) {
+  return static_cast<uint32_t>(m * static_cast<int64_t>(row_bytes)) & 15u;
+}
+
 // Threads of a worker, workers of a CTA, stages, and the grid for M rows whose inputs take
-// `bytes` a row.  stages = 0: the rows do not fit.
+// `bytes` a stage.  stages = 0: the rows do not fit.
 struct RingShape {
   int G, workers, stages;
   unsigned grid;
   size_t smem;
 };
-inline RingShape ring_shape(int64_t M, int64_t K, size_t bytes, int regs, int n = kRingN) {
+inline RingShape ring_shape(int64_t M, int64_t K, size_t bytes, int regs, int n) {
   RingShape s{};
   const int64_t lanes = (K + kActBlock - 1) / kActBlock * (kActLanes / n);
   if (lanes < 16 || lanes > 512) return s;   // under half a warp busy, or over the registers
@@ -42,9 +79,10 @@ inline RingShape ring_shape(int64_t M, int64_t K, size_t bytes, int regs, int n 
     s.stages = 0;
     return s;
   }
-  s.smem = s.workers * s.stages * bytes;
+  s.smem = s.workers * s.stages * bytes + kRingPad;
   const int64_t want = (M + s.workers - 1) / s.workers;
-  s.grid = static_cast<unsigned>(std::min<int64_t>(want, static_cast<int64_t>(ctas) * device_sm_count()));
+  const int64_t most = (static_cast<int64_t>(ctas) * device_sm_count() + 1) / 2 * 2;
+  s.grid = static_cast<unsigned>(std::min(want, most));
   return s;
 }
 
@@ -61,10 +99,88 @@ __device__ __forceinline__ float worker_sum(float v, int G, float* red, int turn
   return s;
 }
 
+// The row's length, such that what follows from it is computed where it is used: the pair layout's
+// bounds, kept for every value across the rows, would take the registers that the rows need.
+__device__ __forceinline__ int not_kept(int64_t K) {
+  int k = static_cast<int>(K);
+  asm volatile("" : "+r"(k));
+  return k;
+}
+
+// Chunk u of a worker's thread t: a block's chunks lie in a thread (kVec), or side by side in 16
+// threads, whose pairs are then next to each other.
+template <bool kVec, int kN>
+__device__ __forceinline__ auto ring_chunk(int t, int G, int u) {
+  if constexpr (kVec) return chunk_of(t, kN, u);
+  else return t + u * G;
+}
+
 // 8 values of chunk c from a row in shared memory (zeros past the row's end).
-template <typename T>
-__device__ __forceinline__ void ring8(const uint8_t* row, int64_t c, int64_t K, float (&v)[8]) {
-  load8<T, true>(reinterpret_cast<const T*>(row), c, K, v);
+template <typename T, bool kVec, typename I>
+__device__ __forceinline__ void ring8(const uint8_t* row, I c, I K, float (&v)[8], int p) {
+  const T* r = reinterpret_cast<const T*>(row);
+  if constexpr (kVec) {
+    load8<T, true>(r, c, K, v);
+  } else {
+    const PairAt<I> q(c, K, p);
+    if (q.left > 0) load_pairs(r, q, v);
+    if (q.left < kActBlock) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = q.feature(j) < q.left ? v[j] : 0.0f;
+    }
+  }
+}
+
+// 8 codes of chunk c (zeros past the row's end).
+template <bool kVec, typename I>
+__device__ __forceinline__ uint2 ring_codes(const uint8_t* row, I c, I K, int p) {
+  const int8_t* r = reinterpret_cast<const int8_t*>(row);
+  if constexpr (kVec) {
+    return load_codes<true>(r, c, K);
+  } else {
+    const PairAt<I> q(c, K, p);
+    uint2 w = q.left > 0 ? load_code_pairs(r, q) : make_uint2(0, 0);
+    if (q.left < kActBlock) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (q.feature(j) >= q.left) (j < 4 ? w.x : w.y) &= ~(0xffu << (8 * (j & 3)));
+    }
+    return w;
+  }
+}
+
+// Quantizes and stores the chunks t + u G of row m: kN = 2 or 4 blocks a half warp.  Lanes 16 / kN of
+// it come to hold one block's largest magnitude (exchanges of halves, then of whole values, for what
+// kN reductions one by one take four each), find its scale and pass it on.
+template <int kN>
+__device__ __forceinline__ void store_ring_blocks(const Act8View& a, int64_t m, int64_t row, int t, int G, int K, int p,
+                                                  const float (&v)[kN][8], int* status) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  constexpr int kOwn = kActLanes / kN;
+  float k[kN];
+#pragma unroll
+  for (int u = 0; u < kN; ++u) k[u] = chunk_amax(v[u], 0.0f);
+#pragma unroll
+  for (int o = 8, n = kN / 2; n > 0; o /= 2, n /= 2)
+#pragma unroll
+    for (int u = 0; u < n; ++u) {
+      const float keep = t & o ? k[u + n] : k[u], give = t & o ? k[u] : k[u + n];
+      k[u] = max_abs_nan(keep, __shfl_xor_sync(kAll, give, o));
+    }
+#pragma unroll
+  for (int o = kOwn / 2; o > 0; o /= 2) k[0] = max_abs_nan(k[0], __shfl_xor_sync(kAll, k[0], o));
+  const BlockScale s(k[0]);
+  const int own = t / kActLanes + t % kActLanes / kOwn * (G / kActLanes);
+  if (t % kOwn == 0 && own * kActBlock < K) {
+    a.scales[m * ((K + kActBlock - 1) / kActBlock) + own] = s.scale;
+    if (s.bad) atomicCAS(status, 0, static_cast<int>(NF4_ERR_NONFINITE));
+  }
+  const float inv = s.bad ? -1.0f : s.inv;
+#pragma unroll
+  for (int u = 0; u < kN; ++u) {
+    const float i = __shfl_sync(kAll, inv, (t & 16) + kOwn * u);
+    store_codes<false>(a.codes + row, t + u * G, K, codes_of(v[u], i, i < 0.0f), p);
+  }
 }
 
 }  // namespace qnf4

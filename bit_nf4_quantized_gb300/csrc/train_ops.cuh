@@ -8,10 +8,13 @@
 // the scale NaN, so that everything read from it is NaN, and sets NF4_ERR_NONFINITE.
 //
 // Layout shared by the kernels: a row is cut in chunks of 8 values, 16 chunks a block.  With
-// K % 8 == 0 every row is 16-byte aligned and a chunk is contiguous (kVec: 16-byte accesses);
-// otherwise chunk i of a block takes features i, i + 16, ... of it, so that neighbouring lanes'
-// narrow accesses stay within the same sectors.  A thread may hold n = 1, 2 or 4 chunks of one
-// block, 16 / n lanes then sharing it (chunk_of): the block's scale costs two divisions a lane.
+// K % 8 == 0 every row is 16-byte aligned and a chunk is contiguous (kVec: 16-byte accesses).
+// Otherwise a chunk is four pairs of features, each one aligned access (8 bytes of floats, 4 of
+// 16-bit elements, 2 of codes), neighbouring chunks' pairs next to each other.  Where a row starts
+// at an odd element (p = 1) the pairs begin one feature earlier, and the feature before the block's
+// first, which belongs to the block before, is replaced by the block's last.  A thread may hold
+// n = 1, 2 or 4 chunks of one block, 16 / n lanes then sharing it (chunk_of): the block's scale costs
+// two divisions a lane.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -78,6 +81,9 @@ size_t act8_grad_ws_bytes(int64_t M, int64_t K, int r);
 cudaError_t launch_act8_grad(const ActGradArgs& a, void* ws, cudaStream_t st);
 
 // ---- device helpers -----------------------------------------------------------------------
+// Parity of row m's first element in a [M][K] tensor.
+__device__ __forceinline__ int row_parity(int64_t m, int64_t K) { return static_cast<int>(m & K & 1); }
+
 template <typename T>
 struct Elem;
 template <>
@@ -96,10 +102,71 @@ struct Elem<__half> {
   static __device__ __forceinline__ __half from(float v) { return __float2half_rn(v); }
 };
 
-// The 8 values of chunk c (16 chunks a block) of a row of K: zeros past the row's end.
-template <typename T, bool kVec>
-__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t K, float (&v)[8]) {
-  if (kVec) {
+// The pair layout's features of chunk c, counted from the block's first one (`base`): values 2u and
+// 2u + 1 are at + 32 u and the next one, except value 0 of a chunk with at = -1, which is the
+// block's last feature.  `left`: the block's features inside the row.
+template <typename I>
+struct PairAt {
+  I base;
+  int at, left;
+  __device__ __forceinline__ PairAt(I c, I K, int p)
+      : base((c / kActLanes) * kActBlock), at(2 * static_cast<int>(c % kActLanes) - p),
+        left(static_cast<int>(max(min(K - base, static_cast<I>(kActBlock)), static_cast<I>(0)))) {}
+  __device__ __forceinline__ int feature(int j) const {   // value j's, in the block
+    return j == 0 && at < 0 ? kActBlock - 1 : at + 32 * (j / 2) + j % 2;
+  }
+};
+
+// Two neighbouring elements as one access.
+template <typename T>
+struct Pair {
+  using Word = uint32_t;
+};
+template <>
+struct Pair<float> {
+  using Word = float2;
+};
+__device__ __forceinline__ float2 unpack2(float2 w, float) { return w; }
+__device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, __half) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ float2 pack2(float a, float b, float) { return make_float2(a, b); }
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A pair layout's chunk, from whole pairs (an odd row's first one starts with the last element of the
+// row before).
+template <typename T, typename I>
+__device__ __forceinline__ void load_pairs(const T* row, const PairAt<I>& q, float (&v)[8]) {
+  using Word = typename Pair<T>::Word;
+  const Word* src = reinterpret_cast<const Word*>(row + q.base + q.at);
+  Word w[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) w[u] = src[16 * u];
+  T last{};
+  if (q.at < 0) last = row[q.base + kActBlock - 1];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const float2 f = unpack2(w[u], T{});
+    v[2 * u] = f.x, v[2 * u + 1] = f.y;
+  }
+  if (q.at < 0) v[0] = Elem<T>::to(last);
+}
+
+// The 8 values of chunk c (16 chunks a block) of a row of K: zeros past the row's end.  p: parity
+// of the row's start (row_parity; kVec: unused).
+template <typename T, bool kVec, typename I>
+__device__ __forceinline__ void load8(const T* row, I c, I K, float (&v)[8], int p = 0) {
+  if constexpr (kVec) {
     alignas(16) T raw[8];
     if (c * 8 < K) {
       const uint4* src = reinterpret_cast<const uint4*>(row + c * 8);
@@ -112,15 +179,19 @@ __device__ __forceinline__ void load8(const T* row, int64_t c, int64_t K, float 
       for (int j = 0; j < 8; ++j) v[j] = 0.0f;
     }
   } else {
-    const int64_t e = (c / kActLanes) * kActBlock + c % kActLanes;
+    const PairAt<I> q(c, K, p);
+    if (q.left == kActBlock) {
+      load_pairs(row, q, v);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = e + 16 * j < K ? Elem<T>::to(row[e + 16 * j]) : 0.0f;
+      for (int j = 0; j < 8; ++j) v[j] = q.feature(j) < q.left ? Elem<T>::to(row[q.base + q.feature(j)]) : 0.0f;
+    }
   }
 }
 
-template <typename T, bool kVec>
-__device__ __forceinline__ void store8(T* row, int64_t c, int64_t K, const float (&v)[8]) {
-  if (kVec) {
+template <typename T, bool kVec, typename I>
+__device__ __forceinline__ void store8(T* row, I c, I K, const float (&v)[8], int p = 0) {
+  if constexpr (kVec) {
     if (c * 8 < K) {
       alignas(16) T raw[8];
 #pragma unroll
@@ -130,26 +201,63 @@ __device__ __forceinline__ void store8(T* row, int64_t c, int64_t K, const float
       if (sizeof(T) == 4) dst[1] = *reinterpret_cast<uint4*>(raw + 4);
     }
   } else {
-    const int64_t e = (c / kActLanes) * kActBlock + c % kActLanes;
+    const PairAt<I> q(c, K, p);
+    if (q.left == kActBlock) {
+      using Word = typename Pair<T>::Word;
+      Word* dst = reinterpret_cast<Word*>(row + q.base + q.at);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (e + 16 * j < K) row[e + 16 * j] = Elem<T>::from(v[j]);
+      for (int u = 1; u < 4; ++u) dst[16 * u] = pack2(v[2 * u], v[2 * u + 1], T{});
+      if (q.at < 0) {
+        row[q.base + kActBlock - 1] = Elem<T>::from(v[0]);
+        row[q.base] = Elem<T>::from(v[1]);
+      } else {
+        dst[0] = pack2(v[0], v[1], T{});
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (q.feature(j) < q.left) row[q.base + q.feature(j)] = Elem<T>::from(v[j]);
+    }
   }
 }
 
-// A lane's 8 codes, packed in feature order (byte j: value j).
-template <bool kVec>
-__device__ __forceinline__ uint2 load_codes(const int8_t* row, int64_t c, int64_t K) {
+// The same features of a [K] vector, whose start is even whatever the row's is.
+template <bool kVec, typename I>
+__device__ __forceinline__ void load_vector8(const float* w, I c, I K, float (&v)[8], int p) {
+  if (kVec || p == 0) {
+    load8<float, kVec>(w, c, K, v);
+  } else {
+    const PairAt<I> q(c, K, p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = q.feature(j) < q.left ? w[q.base + q.feature(j)] : 0.0f;
+  }
+}
+
+template <typename I>
+__device__ __forceinline__ uint2 load_code_pairs(const int8_t* row, const PairAt<I>& f) {
+  const uint16_t* src = reinterpret_cast<const uint16_t*>(row + f.base + f.at);
+  uint2 q = make_uint2(__byte_perm(src[0], src[16], 0x5410), __byte_perm(src[32], src[48], 0x5410));
+  if (f.at < 0) q.x = (q.x & 0xffffff00u) | static_cast<uint8_t>(row[f.base + kActBlock - 1]);
+  return q;
+}
+
+// A lane's 8 codes, packed in order (byte j: value j).
+template <bool kVec, typename I>
+__device__ __forceinline__ uint2 load_codes(const int8_t* row, I c, I K, int p = 0) {
   uint2 q = make_uint2(0, 0);
-  if (kVec) {
+  if constexpr (kVec) {
     if (c * 8 < K) q = *reinterpret_cast<const uint2*>(row + c * 8);
   } else {
-    const int64_t e = (c / kActLanes) * kActBlock + c % kActLanes;
+    const PairAt<I> f(c, K, p);
+    if (f.left == kActBlock) {
+      q = load_code_pairs(row, f);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t b = e + 16 * j < K ? static_cast<uint8_t>(row[e + 16 * j]) : 0u;
-      if (j < 4) q.x |= b << (8 * j);
-      else q.y |= b << (8 * (j - 4));
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t b = f.feature(j) < f.left ? static_cast<uint8_t>(row[f.base + f.feature(j)]) : 0u;
+        if (j < 4) q.x |= b << (8 * j);
+        else q.y |= b << (8 * (j - 4));
+      }
     }
   }
   return q;
@@ -184,53 +292,78 @@ struct Quantized {
   float scale;
   bool bad;
 };
+struct BlockScale {
+  float scale, inv;
+  bool bad;
+  __device__ __forceinline__ explicit BlockScale(float amax) {
+    bad = !(amax < INFINITY);
+    const bool live = amax >= kActTiny && !bad;
+    inv = live ? 127.0f / amax : 0.0f;
+    scale = bad ? __int_as_float(0x7fc00000) : live ? amax / 127.0f : 0.0f;
+  }
+};
+__device__ __forceinline__ float chunk_amax(const float (&v)[8], float amax) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) amax = max_abs_nan(amax, v[j]);
+  return amax;
+}
+__device__ __forceinline__ uint2 codes_of(const float (&v)[8], float inv, bool bad) {
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[j], inv), 12582912.0f));
+  const uint32_t x = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+  const uint32_t y = __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410);
+  return bad ? make_uint2(0, 0) : make_uint2(x, y);
+}
 template <int kN>
 __device__ __forceinline__ Quantized<kN> quantize_block(const float (&v)[kN][8]) {
   float amax = 0.0f;
 #pragma unroll
-  for (int u = 0; u < kN; ++u)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) amax = max_abs_nan(amax, v[u][j]);
+  for (int u = 0; u < kN; ++u) amax = chunk_amax(v[u], amax);
 #pragma unroll
   for (int o = kActLanes / kN / 2; o > 0; o >>= 1) amax = max_abs_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const BlockScale s(amax);
   Quantized<kN> q;
-  q.bad = !(amax < INFINITY);
-  const bool live = amax >= kActTiny && !q.bad;
-  const float inv = live ? 127.0f / amax : 0.0f;
-  q.scale = q.bad ? __int_as_float(0x7fc00000) : live ? amax / 127.0f : 0.0f;
+  q.bad = s.bad, q.scale = s.scale;
 #pragma unroll
-  for (int u = 0; u < kN; ++u) {
-    uint32_t w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[u][j], inv), 12582912.0f));
-    q.codes[u].x = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
-    q.codes[u].y = __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410);
-    if (q.bad) q.codes[u] = make_uint2(0, 0);
-  }
+  for (int u = 0; u < kN; ++u) q.codes[u] = codes_of(v[u], s.inv, s.bad);
   return q;
 }
 
 // Stores chunk c's codes.
-template <bool kVec>
-__device__ __forceinline__ void store_codes(int8_t* row, int64_t c, int64_t K, uint2 q) {
-  if (kVec) {
+template <bool kVec, typename I>
+__device__ __forceinline__ void store_codes(int8_t* row, I c, I K, uint2 q, int p) {
+  if constexpr (kVec) {
     if (c * 8 < K) *reinterpret_cast<uint2*>(row + c * 8) = q;
   } else {
-    const int64_t e = (c / kActLanes) * kActBlock + c % kActLanes;
+    const PairAt<I> f(c, K, p);
+    if (f.left == kActBlock) {
+      uint16_t* dst = reinterpret_cast<uint16_t*>(row + f.base + f.at);
+      dst[16] = static_cast<uint16_t>(q.x >> 16);
+      dst[32] = static_cast<uint16_t>(q.y);
+      dst[48] = static_cast<uint16_t>(q.y >> 16);
+      if (f.at < 0) {
+        row[f.base + kActBlock - 1] = static_cast<int8_t>(q.x);
+        row[f.base] = static_cast<int8_t>(q.x >> 8);
+      } else {
+        dst[0] = static_cast<uint16_t>(q.x);
+      }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (e + 16 * j < K) row[e + 16 * j] = static_cast<int8_t>((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+      for (int j = 0; j < 8; ++j)
+        if (f.feature(j) < f.left) row[f.base + f.feature(j)] = static_cast<int8_t>((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+    }
   }
 }
 
 // Stores what a thread quantized: its chunks' codes, and the scale from the block's first lane.
 template <bool kVec, int kN>
 __device__ __forceinline__ void store_block(const Act8View& a, int64_t m, int64_t t, int64_t K, const Quantized<kN>& q,
-                                            int* status) {
+                                            int* status, int p = 0) {
   const int64_t b = t / (kActLanes / kN);
   if (b * kActBlock >= K) return;
 #pragma unroll
-  for (int u = 0; u < kN; ++u) store_codes<kVec>(a.codes + m * K, chunk_of(t, kN, u), K, q.codes[u]);
+  for (int u = 0; u < kN; ++u) store_codes<kVec>(a.codes + m * K, chunk_of(t, kN, u), K, q.codes[u], p);
   if (t % (kActLanes / kN) == 0) {
     a.scales[m * ((K + kActBlock - 1) / kActBlock) + b] = q.scale;
     if (q.bad) atomicCAS(status, 0, static_cast<int>(NF4_ERR_NONFINITE));

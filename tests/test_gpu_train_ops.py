@@ -280,6 +280,52 @@ def test_norm_backward_many_rows(lib, K):
     assert qlora.rel_frobenius(_np(dx), wdx) <= 2.0 ** -8
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,K", [(2503, 1025), (1201, 2050), (1600, 1533), (631, 4097), (700, 8195), (331, 10001)])
+def test_norm_rows_off_their_alignment(lib, dtype, M, K):
+    """Rows that start and end inside a 16-byte piece, several a worker: values, in place, and nothing
+    written past the tensors' ends."""
+    rng = _rng(9, M, K)
+    dt, pad = DT[dtype], 64
+
+    def tail(like, n=M * K):
+        flat = torch.full((n + pad,), 77, dtype=like, device=DEV)
+        return flat, flat[:n]
+
+    x, r, dy = (_dev(rng.standard_normal((M, K)), dt) for _ in range(3))
+    w = _dev(1 + 0.2 * rng.standard_normal(K))
+    bufs = {k: tail(dt) for k in ("y", "h", "dx")}
+    y, h, dx = (bufs[k][1].view(M, K) for k in ("y", "h", "dx"))
+    cf, cv = tail(torch.int8)
+    c = b.Act8(cv.view(M, K), torch.empty(M, (K + 127) // 128, device=DEV))
+    _, _, rstd, _ = b.qlora_rms_norm_fwd(x, w, 1e-5, residual=r, y=y, h=h, checkpoint=c)
+    wy, wh, wr, wn = ot.rms_norm_fwd(_np(x), _np(r), _np(w), 1e-5)
+    e = 100 * U
+    near = 2 * U * wr[:, None] * (np.abs(_np(x)) + np.abs(_np(r)))
+    _within(rstd, wr, e * wr, "rstd")
+    _within(y, wy, (U_OUT[dtype] + e) * np.abs(wy) * 1.01 + FLOOR[dtype] + near * np.abs(_np(w)), "y")
+    _within(h, wh, (U_OUT[dtype] + U) * np.abs(wh) * 1.01 + FLOOR[dtype], "h")
+    got = ot.act8_values(c.codes.cpu().numpy(), c.scales.cpu().numpy())
+    step = np.repeat(_np(c.scales), 128, axis=1)[:, :K]
+    assert np.all(np.abs(got - wn) <= 0.5 * step * (1 + 2.0 ** -14) + 2 * e * np.abs(wn) + near)
+    x2, r2 = x.clone(), r.clone()
+    b.qlora_rms_norm_fwd(x2, w, 1e-5, residual=r2, y=x2, h=r2)
+    assert torch.equal(x2, y) and torch.equal(r2, h)
+    for saved, n in ((h, _np(h) * _np(rstd)[:, None]), (c, got)):
+        _, dw = b.qlora_rms_norm_bwd(dy, saved, rstd, w, dresidual=r, dweight=True, dx=dx)
+        wdx, wdw = ot.rms_norm_bwd(_np(dy), n, _np(rstd), _np(w), _np(r))
+        d = np.abs(_np(dy) * _np(w))
+        mag = _np(rstd)[:, None] * (d + np.abs(n) * (d * np.abs(n)).mean(axis=1, keepdims=True)) + np.abs(_np(r))
+        _within(dx, wdx, U_OUT[dtype] * np.abs(wdx) * 1.01 + 2.0 ** -16 * mag + FLOOR[dtype], "dx")
+        _within(dw, wdw, (M + 64) * U * (np.abs(_np(dy)) * np.abs(n)).sum(axis=0), "dweight")
+        once = dx.clone()
+        b.qlora_rms_norm_bwd(dy, saved, rstd, w, dresidual=r, dx=dx)      # a frozen weight's form
+        assert qlora.rel_frobenius(_np(dx), _np(once)) <= U_OUT[dtype]
+    for flat, _ in (*bufs.values(), (cf, cv)):
+        assert (flat[M * K:] == 77).all()
+    _ok()
+
+
 def test_norm_zero_rows_and_in_place(lib):
     w = torch.ones(200, device=DEV)
     x = torch.zeros(3, 200, device=DEV)
