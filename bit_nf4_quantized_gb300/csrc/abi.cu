@@ -282,6 +282,8 @@ WaitSettings take_wait_settings() {
   return WaitSettings{4000000000ull, 0};
 }
 
+bool wait_test_armed() { return g_wait_fault.load() != 0; }
+
 const DecodeTables& decode_tables() { return tables().dec; }
 const EncodeTables& encode_tables() { return tables().enc; }
 

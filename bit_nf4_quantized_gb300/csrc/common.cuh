@@ -107,6 +107,7 @@ struct WaitSettings {
   int skip_stage0;
 };
 WaitSettings take_wait_settings();
+bool wait_test_armed();        // the next contraction with bounded waits is to give up
 
 // Programmatic dependent launch.  Kernels of the bf16 path are launched with
 // programmatic stream serialization: a kernel may start while its predecessor in the

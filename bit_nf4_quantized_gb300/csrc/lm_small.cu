@@ -1,0 +1,476 @@
+// The loss and its gradient in one launch, for few products.
+//
+// lm_loss.cu's launches follow one another (preparation, scores, their repetition, gradient, totals),
+// and at small sizes their latencies are all its time.  Here a cluster of CTAs takes 16 tokens and
+// the whole vocabulary, each CTA a part of it, each of its groups of warps 16 entries at a time:
+// z = x W^T (m16n8k16 products, operands by ldmatrix, W's rows by bulk copies), the group's running
+// maximum m of each token, p = exp(z - m) in 16 bits, acc = acc exp(m_old - m) + p W with the same rows.
+// A warp's z is in the lanes where p is wanted, so groups share nothing until they add their sums,
+// in the CTA and then through the cluster's distributed shared memory, and finish the tokens as
+// lm_finish does.  The mathematics is lm_loss.cu's with m for the reference R: p is at most 1, so no part
+// is ever repeated, and a target's logit is taken as its group meets it.
+//
+// Bound by latency at its smallest, then by what an SM takes in: every CTA reads its part of W for
+// 16 tokens only (8 rows of 512 bytes in 90 ns: a row's copy costs 5 ns and its bytes at 90 GB/s), which
+// limits it to few products (lm_small_plan).
+#include <algorithm>
+#include <mutex>
+
+#include <cuda_fp16.h>
+
+#include "lm_loss.cuh"
+#include "mma_sync.cuh"
+#include "row_ring.cuh"
+
+namespace qnf4 {
+namespace {
+
+constexpr int kTok = 16;              // tokens of a cluster
+constexpr int kRows = 16;             // vocabulary entries of a step
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStagesMax = 4;
+constexpr int kWarpD = 256;           // features a warp sums at most
+constexpr int kClusterMax = 8;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct SmallArgs {
+  int M, V, D, steps, cluster, stages;
+  int64_t ignore;
+  const void* x;
+  const void* W;
+  const int64_t* targets;
+  const float* gscale;
+  int gscale_per_row;
+  float* loss;
+  float* lse;
+  void* dx;
+  int* status;
+};
+
+// Elements from one row of x or W to the next in shared memory: the contraction in pairs of products,
+// and an odd number of 16 bytes, which keeps ldmatrix's 8 rows on different banks.
+__host__ __device__ constexpr int pitch_of(int D) { return (D + 31) / 32 * 32 + 8; }
+__host__ __device__ constexpr int small_smem(int D, int split, int stages) {
+  return 2 * pitch_of(D) * (kTok + kRows * stages * (kWarps / split));
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t at) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if (F16) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <bool F16>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+  if (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// A group of kSplit warps takes steps of 16 entries; each of its warps computes their logits and
+// then sums its 8 kNt features (kNt = 0: no gradient).  A warp's logits are the fragments of its
+// gradient's products, so groups share nothing before the end.
+template <bool F16, int kNt, int kSplit>
+__global__ void __launch_bounds__(kThreads, kNt == 8 ? 2 : 1) lm_small(const SmallArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr bool kGrad = kNt > 0;
+  constexpr int kGroups = kWarps / kSplit, kGroupThreads = 32 * kSplit;
+  __shared__ float group_max[kGroups][kTok], group_sum[kGroups][kTok];
+  __shared__ float own_z[kTok], tok_max[kTok], tok_sum[kTok];
+  __shared__ float factor[kGroups > kClusterMax ? kGroups : kClusterMax][kTok];
+  __shared__ float2 coef[kTok];
+  __shared__ uint64_t bars[kGroups][kStagesMax], x_bar;
+  __shared__ int gave_up;
+  const int thread = threadIdx.x, warp = thread >> 5, lane = thread & 31, g = lane >> 2, c = lane & 3;
+  const int group = warp / kSplit, part = warp % kSplit, in_group = thread % kGroupThreads;
+  const int C = a.cluster, rank = static_cast<int>(blockIdx.x) % C;
+  const int t0 = static_cast<int>(blockIdx.x) / C * kTok;
+  const int pitch = pitch_of(a.D), d8 = a.D / 8, pairs = (a.D + 31) / 32;
+  const uint32_t step_bytes = 2 * kRows * pitch;
+  uint8_t* const mine = smem + 2 * kTok * pitch + group * a.stages * step_bytes;
+  const uint32_t xs = tc::smem_u32(smem), wbuf = tc::smem_u32(mine);
+  const int first = rank * a.steps / C + group, last = (rank + 1) * a.steps / C;
+  const uint8_t* W = static_cast<const uint8_t*>(a.W);
+  auto group_sync = [&] {
+    if (kSplit == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory");
+  };
+
+  const uint32_t bar = tc::smem_u32(bars[group]), row_bytes = 2 * a.D;
+  if (in_group == 0)
+    for (int q = 0; q < a.stages; ++q) tc::mbar_init(bar + 8 * q, 1);
+  if (thread == 0) gave_up = 0, tc::mbar_init(tc::smem_u32(&x_bar), 1);
+  if (thread < kTok) own_z[thread] = 0.0f;
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncthreads();
+  pdl_allow_next();
+  pdl_wait();
+
+  // a step's rows, a copy each, by the group's first warp; rows past the vocabulary are zeros
+  auto load_step = [&](int step, int stage) {
+    if (part != 0) return;
+    const int v0 = step * kRows, rows = min(kRows, a.V - v0);
+    if (rows < kRows)
+      for (int i = lane; i < (kRows - rows) * d8; i += 32)
+        *reinterpret_cast<uint4*>(mine + stage * step_bytes + 2 * ((rows + i / d8) * pitch + 8 * (i % d8))) = make_uint4(0, 0, 0, 0);
+    if (lane == 0) tc::mbar_expect_tx(bar + 8 * stage, rows * row_bytes);
+    __syncwarp();
+    if (lane < rows)
+      bulk_copy(wbuf + stage * step_bytes + 2 * lane * pitch, W + static_cast<int64_t>(v0 + lane) * row_bytes, row_bytes,
+                bar + 8 * stage);
+  };
+  for (int q = 0; q < a.stages; ++q)
+    if (first + q * kGroups < last) load_step(first + q * kGroups, q);
+  if (warp == kWarps - 1) {     // the tokens; zeros past the last
+    const int rows = min(kTok, a.M - t0);
+    for (int i = lane; i < (kTok - rows) * d8; i += 32)
+      *reinterpret_cast<uint4*>(smem + 2 * ((rows + i / d8) * pitch + 8 * (i % d8))) = make_uint4(0, 0, 0, 0);
+    if (lane == 0) tc::mbar_expect_tx(tc::smem_u32(&x_bar), rows * row_bytes);
+    __syncwarp();
+    if (lane < rows)
+      bulk_copy(xs + 2 * lane * pitch, static_cast<const uint8_t*>(a.x) + static_cast<int64_t>(t0 + lane) * row_bytes, row_bytes,
+                tc::smem_u32(&x_bar));
+  }
+  // the target of token t0 + k, or -1 where it does not count
+  auto target_of = [&](int k) {
+    const int64_t given = t0 + k < a.M ? a.targets[t0 + k] : a.ignore;
+    return given >= 0 && given < a.V && given != a.ignore ? static_cast<int>(given) : -1;
+  };
+  const int ty0 = target_of(g), ty1 = target_of(g + 8);
+  // zeros between D and the last pair of products' end
+  for (int r = thread; r < kTok + kRows * a.stages * kGroups; r += kThreads)
+    for (int k = d8; k < 4 * pairs; ++k) *reinterpret_cast<uint4*>(smem + 2 * (r * pitch + 8 * k)) = make_uint4(0, 0, 0, 0);
+  float m0 = -INFINITY, m1 = -INFINITY, s0 = 0.0f, s1 = 0.0f;     // of tokens g and g + 8, in powers of two
+  float acc[kGrad ? kNt : 1][4];
+#pragma unroll
+  for (int i = 0; i < (kGrad ? kNt : 1); ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[i][q] = 0.0f;
+  // ldmatrix: x's and, transposed, W's 16 x 16 (rows, then the upper 8 columns); W's entries (rows 0-7,
+  // their upper 8 columns, rows 8-15)
+  const uint32_t x_at = xs + 2 * ((lane & 15) * pitch + 8 * (lane >> 4));
+  const uint32_t z_at = 2 * (((lane & 7) + 8 * (lane >> 4)) * pitch + 8 * (lane >> 3 & 1));
+  const uint32_t d_at = 2 * ((lane & 15) * pitch + 8 * (lane >> 4) + kWarpD * part);
+  __syncthreads();              // the zeros are there
+  tc::mbar_wait(tc::smem_u32(&x_bar), 0, &gave_up, a.status);
+
+  int stage = 0;
+  uint32_t phase = 0;
+  for (int step = first; step < last; step += kGroups) {
+    // (a wait that gives up leaves the loop's shape as it is: the later ones return at once)
+    tc::mbar_wait(bar + 8 * stage, phase, &gave_up, a.status);
+    const uint32_t w = wbuf + stage * step_bytes;
+    float z[4][2][4] = {};        // [product modulo 4][entries 0-7 or 8-15]: short chains
+    for (int k = 0; k < pairs; k += 2) {
+      uint32_t b[4][4], p[4][4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        if (h < 2 || k + 1 < pairs) {
+          ldmatrix4(b[h], w + z_at + 64 * k + 32 * h);
+          ldmatrix4(p[h], x_at + 64 * k + 32 * h);
+        }
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        if (h < 2 || k + 1 < pairs) {
+          mma16816<F16>(z[h][0], p[h][0], p[h][1], p[h][2], p[h][3], b[h][0], b[h][1]);
+          mma16816<F16>(z[h][1], p[h][0], p[h][1], p[h][2], p[h][3], b[h][2], b[h][3]);
+        }
+    }
+    const int v = step * kRows + 2 * c;    // this lane's entries v, v + 1, v + 8, v + 9 of tokens g, g + 8
+    float n0 = m0, n1 = m1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        z[0][h][q] = (z[0][h][q] + z[1][h][q]) + (z[2][h][q] + z[3][h][q]);
+        if (v + 8 * h + (q & 1) < a.V) (q < 2 ? n0 : n1) = fmaxf(q < 2 ? n0 : n1, z[0][h][q] * kLog2e);
+      }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
+      n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
+    }
+    // (no logit above -inf yet: any reference will do)
+    const float r0 = n0 == -INFINITY ? 0.0f : n0, r1 = n1 == -INFINITY ? 0.0f : n1;
+    const float f0 = m0 == n0 ? 1.0f : exp2f(m0 - r0), f1 = m1 == n1 ? 1.0f : exp2f(m1 - r1);
+    m0 = n0, m1 = n1;
+    float e[2][4], e0 = 0.0f, e1 = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int entry = v + 8 * h + (q & 1);
+        const float x = exp2f(fmaf(z[0][h][q], kLog2e, -(q < 2 ? r0 : r1)));
+        const bool own = entry == (q < 2 ? ty0 : ty1);
+        if (own && part == 0) own_z[q < 2 ? g : g + 8] = z[0][h][q];
+        e[h][q] = entry < a.V && !own ? x : 0.0f;
+        (q < 2 ? e0 : e1) += e[h][q];
+      }
+    s0 = fmaf(s0, f0, e0);
+    s1 = fmaf(s1, f1, e1);
+    if (kGrad) {
+      if (__any_sync(0xffffffffu, f0 != 1.0f || f1 != 1.0f)) {
+#pragma unroll
+        for (int i = 0; i < kNt; ++i) acc[i][0] *= f0, acc[i][1] *= f0, acc[i][2] *= f1, acc[i][3] *= f1;
+      }
+      const uint32_t p0 = pack16<F16>(e[0][0], e[0][1]), p1 = pack16<F16>(e[0][2], e[0][3]);
+      const uint32_t p2 = pack16<F16>(e[1][0], e[1][1]), p3 = pack16<F16>(e[1][2], e[1][3]);
+#pragma unroll
+      for (int i = 0; i < kNt; i += 4) {
+        if (kWarpD * part + 8 * i >= a.D) break;      // (32 features, the last ones' zeros with them)
+        uint32_t y[2][4];
+        ldmatrix4_trans(y[0], w + d_at + 16 * i);
+        ldmatrix4_trans(y[1], w + d_at + 16 * i + 32);
+        mma16816<F16>(acc[i], p0, p1, p2, p3, y[0][0], y[0][1]);
+        mma16816<F16>(acc[i + 1], p0, p1, p2, p3, y[0][2], y[0][3]);
+        mma16816<F16>(acc[i + 2], p0, p1, p2, p3, y[1][0], y[1][1]);
+        mma16816<F16>(acc[i + 3], p0, p1, p2, p3, y[1][2], y[1][3]);
+      }
+    }
+    group_sync();                 // the step's rows have been read
+    if (step + a.stages * kGroups < last) {
+      load_step(step + a.stages * kGroups, stage);
+      if (step + (a.stages + 1) * kGroups >= last) group_sync();     // a last step's zeros
+    }
+    if (++stage == a.stages) stage = 0, phase ^= 1u;
+  }
+  if (gave_up && thread == 0) tc::mbar_drain(tc::smem_u32(&x_bar), 0);
+  if (gave_up && in_group == 0)
+    for (int q = 0; q < a.stages; ++q) {     // let copies in flight land before the sums take their place
+      tc::mbar_drain(bar + 8 * stage, phase);
+      if (++stage == a.stages) stage = 0, phase ^= 1u;
+    }
+  group_sync();
+
+  // the groups' sums, [token][feature] in their steps' place, then the CTA's in the first's
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+    s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+  }
+  if (part == 0 && c == 0) {
+    group_max[group][g] = m0, group_max[group][g + 8] = m1;
+    group_sum[group][g] = s0, group_sum[group][g + 8] = s1;
+  }
+  if (kGrad) {
+    float* s = reinterpret_cast<float*>(mine);
+#pragma unroll
+    for (int i = 0; i < kNt; ++i) {
+      const int d = kWarpD * part + 8 * i + 2 * c;
+      if (d >= a.D) break;
+      *reinterpret_cast<float2*>(s + g * a.D + d) = make_float2(acc[i][0], acc[i][1]);
+      *reinterpret_cast<float2*>(s + (g + 8) * a.D + d) = make_float2(acc[i][2], acc[i][3]);
+    }
+  }
+  __syncthreads();
+  if (thread < kTok) {
+    float m = -INFINITY, s = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) m = fmaxf(m, group_max[q][thread]);
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) {
+      const float f = group_max[q][thread] == m ? 1.0f : group_max[q][thread] == -INFINITY ? 0.0f : exp2f(group_max[q][thread] - m);
+      factor[q][thread] = f;
+      s += group_sum[q][thread] * f;
+    }
+    tok_max[thread] = m, tok_sum[thread] = s;
+  }
+  __syncthreads();
+  float* const sums = reinterpret_cast<float*>(smem + 2 * kTok * pitch);
+  if (kGrad) {
+    const int d4 = a.D / 4;
+    for (int i = thread; i < kTok * d4; i += kThreads) {
+      const int k = i / d4;
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int q = 0; q < kGroups; ++q) {
+        const float f = factor[q][k];
+        const float4 u = *reinterpret_cast<const float4*>(reinterpret_cast<const uint8_t*>(sums) + q * a.stages * step_bytes + 16 * i);
+        s.x = fmaf(u.x, f, s.x), s.y = fmaf(u.y, f, s.y), s.z = fmaf(u.z, f, s.z), s.w = fmaf(u.w, f, s.w);
+      }
+      *reinterpret_cast<float4*>(sums + 4 * i) = s;
+    }
+  }
+  if (C > 1) tc::cluster_sync();
+  else __syncthreads();
+
+  // the cluster's: each CTA takes the tokens' totals, then its share of dx
+  if (thread < kTok) {
+    const uint32_t at_own = tc::smem_u32(own_z + thread);
+    const uint32_t at_max = tc::smem_u32(tok_max + thread), at_sum = tc::smem_u32(tok_sum + thread);
+    float m[kClusterMax], s[kClusterMax], z = 0.0f;
+#pragma unroll
+    for (int y = 0; y < kClusterMax; ++y)
+      if (y < C) {
+        m[y] = ld_cluster(tc::mapa_shared(at_max, y)), s[y] = ld_cluster(tc::mapa_shared(at_sum, y));
+        z += ld_cluster(tc::mapa_shared(at_own, y));        // (of the one CTA that met the target)
+      }
+    float ref = z * kLog2e;
+#pragma unroll
+    for (int y = 0; y < kClusterMax; ++y)
+      if (y < C) ref = fmaxf(ref, m[y]);
+    float others = 0.0f;
+#pragma unroll
+    for (int y = 0; y < kClusterMax; ++y)
+      if (y < C) {
+        const float f = m[y] == ref ? 1.0f : m[y] == -INFINITY ? 0.0f : exp2f(m[y] - ref);
+        factor[y][thread] = f;
+        others += s[y] * f;
+      }
+    const int64_t given = t0 + thread < a.M ? a.targets[t0 + thread] : a.ignore;
+    const bool live = target_of(thread) >= 0;
+    if (!live && given != a.ignore && rank == 0) atomicCAS(a.status, 0, static_cast<int>(NF4_ERR_ARG));
+    const float d = fmaf(z, kLog2e, -ref), own = exp2f(d), total = others + own;     // as in lm_finish
+    const float l = d > -28.0f ? log1pf(others / own) : fmaf(-kLn2, d, logf(total));
+    if (rank == 0 && t0 + thread < a.M) {
+      a.loss[t0 + thread] = live ? l : 0.0f;
+      if (a.lse != nullptr) a.lse[t0 + thread] = live ? z + l : 0.0f;
+    }
+    const float gs = live ? (a.gscale == nullptr ? 1.0f : a.gscale[a.gscale_per_row ? t0 + thread : 0]) : 0.0f;
+    coef[thread] = make_float2(gs / total, gs * (others / total));
+  }
+  if (kGrad) {
+    __syncthreads();
+    for (int i = rank * kThreads + thread; i < kTok * d8; i += C * kThreads) {
+      const int k = i / d8, d = i - k * d8;
+      if (t0 + k >= a.M) break;
+      uint4 o = make_uint4(0, 0, 0, 0);
+      const int y0 = target_of(k);
+      if (y0 >= 0) {
+        const uint4 w = reinterpret_cast<const uint4*>(W + 2 * static_cast<int64_t>(y0) * a.D)[d];
+        const uint32_t at = tc::smem_u32(sums + 8 * i);
+        float s[8] = {};
+#pragma unroll 4
+        for (int y = 0; y < C; ++y) {
+          const uint32_t from = tc::mapa_shared(at, y);
+          const float f = factor[y][k];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float4 u;
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(u.x), "=f"(u.y), "=f"(u.z), "=f"(u.w)
+                         : "r"(from + 16 * h)
+                         : "memory");
+            s[4 * h] = fmaf(u.x, f, s[4 * h]), s[4 * h + 1] = fmaf(u.y, f, s[4 * h + 1]);
+            s[4 * h + 2] = fmaf(u.z, f, s[4 * h + 2]), s[4 * h + 3] = fmaf(u.w, f, s[4 * h + 3]);
+          }
+        }
+        const float2 q = coef[k];
+        const float2 w0 = unpack16<F16>(w.x), w1 = unpack16<F16>(w.y), w2 = unpack16<F16>(w.z), w3 = unpack16<F16>(w.w);
+        o.x = pack16<F16>(q.x * s[0] - q.y * w0.x, q.x * s[1] - q.y * w0.y);
+        o.y = pack16<F16>(q.x * s[2] - q.y * w1.x, q.x * s[3] - q.y * w1.y);
+        o.z = pack16<F16>(q.x * s[4] - q.y * w2.x, q.x * s[5] - q.y * w2.y);
+        o.w = pack16<F16>(q.x * s[6] - q.y * w3.x, q.x * s[7] - q.y * w3.y);
+      }
+      reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.dx) + 2 * static_cast<int64_t>(t0 + k) * a.D)[d] = o;
+    }
+  }
+  if (C > 1) tc::cluster_sync();          // no CTA leaves while another reads its sums
+}
+
+constexpr int kSmemMax = 220 * 1024;
+
+int stages_of(int D, int split) {
+  int s = kStagesMax;
+  while (s > 2 && small_smem(D, split, s) > kSmemMax) --s;
+  return s;
+}
+int split_of(int D) { return D <= kWarpD ? 1 : D <= 2 * kWarpD ? 2 : 4; }
+template <bool F16>
+auto kernel_of(int D, bool grad) {
+  if (!grad) return lm_small<F16, 0, 1>;
+  return D <= 64 ? lm_small<F16, 8, 1> : D <= 128 ? lm_small<F16, 16, 1> : D <= kWarpD ? lm_small<F16, 32, 1>
+         : D <= 2 * kWarpD ? lm_small<F16, 32, 2> : lm_small<F16, 32, 4>;
+}
+
+}  // namespace
+
+// The cluster with the least estimated time in microseconds, if that is less than the launches of
+// lm_loss.cu take.  Here: a start and an end, and `steps` steps of each group one after another, as often
+// as the clusters do not fit the SMs at once (large ones leave some unused).  There: the launches'
+// latencies, the products, and the gradient's fp32 sums.  Measured with a gradient, here and there:
+// 1 x 300 x 64 6.6 and 12.4, 5 x 1038 x 144 10.1 and 13.7, 121 x 1084 x 248 12.3 and 22.6,
+// 650 x 908 x 240 14.7 and 25.4, 4096 x 1000 x 64 16 and 29, 300 x 2000 x 512 28.8 and 26.4,
+// 785 x 11051 x 600 438 and 49; without one, 1 x 300 x 64 4.9 and 9.0, 650 x 908 x 240 10.5 and 10.3.
+LmSmallPlan lm_small_plan(int64_t M, int64_t V, int64_t D, bool grad) {
+  LmSmallPlan best{0};
+  if (D > (grad ? kSmallMaxD : kWarpD) || M > (1 << 16) || V > (1 << 20)) return best;
+  if (wait_test_armed()) return best;        // nothing here waits long enough to give up
+  const double m = static_cast<double>(M), v = static_cast<double>(V), d = static_cast<double>(D);
+  double there = grad ? (M <= kLmStreamMaxM ? 12.0 + 1.2e-6 * v * d : 20.0 + 4.0 * m * v * d / 0.8e9 + 3.3e-6 * m * d)
+                      : (M <= kLmStreamMaxM ? 8.2 + 0.4e-6 * v * d : 8.2 + 0.0013 * m + 2.0 * m * v * d / 1.2e9);
+  there *= 0.95;
+  const int split = grad ? split_of(static_cast<int>(D)) : 1, groups = kWarps / split;
+  const double ends = grad ? 6.0 + 0.0115 * d : 4.0 + 0.006 * d;
+  const double step = !grad ? 0.35 + 0.0043 * d : split == 1 ? 0.35 + 0.0051 * d : 1.0 + 0.00205 * d;
+  const int64_t steps = (V + kRows - 1) / kRows, tiles = (M + kTok - 1) / kTok;
+  const int sms = std::max(1, device_sm_count()), per_sm = D <= 64 ? 2 : 1;
+  for (int c = 1; c <= kClusterMax && c <= steps; c *= 2) {
+    const int64_t fit = std::max<int64_t>(1, static_cast<int64_t>(sms) * per_sm * (c <= 2 ? 16 : c == 4 ? 15 : 13) / 16 / c);
+    const int64_t rounds = (tiles + fit - 1) / fit, each = ((steps + c - 1) / c + groups - 1) / groups;
+    const double crowd = tiles * c > sms ? 1.4 : 1.0;
+    const double t = static_cast<double>(rounds) * (ends + crowd * step * static_cast<double>(each)) + (c > 1 ? 0.5 : 0.0);
+    if (t < there) there = t, best.cluster = c;
+  }
+  return best;
+}
+
+cudaError_t launch_lm_small(const LmLossArgs& a, const LmSmallPlan& plan, const void* W, int* status, cudaStream_t st) {
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [] {
+    auto allow = [](auto* f) {
+      if (err == cudaSuccess) err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    };
+    for (const int D : {64, 128, 256, 512, 1024}) allow(kernel_of<false>(D, true)), allow(kernel_of<true>(D, true));
+    allow(kernel_of<false>(64, false)), allow(kernel_of<true>(64, false));
+  });
+  if (err != cudaSuccess) return err;
+  const int D = static_cast<int>(a.D);
+  SmallArgs s{};
+  s.M = static_cast<int>(a.M);
+  s.V = static_cast<int>(a.V);
+  s.D = D;
+  s.steps = static_cast<int>((a.V + kRows - 1) / kRows);
+  s.cluster = plan.cluster;
+  const int split = a.dx != nullptr ? split_of(D) : 1;
+  s.stages = stages_of(D, split);
+  s.ignore = a.ignore_index;
+  s.x = a.x;
+  s.W = W;
+  s.targets = a.targets;
+  s.gscale = a.grad_scale;
+  s.gscale_per_row = a.grad_scale_per_row;
+  s.loss = a.loss;
+  s.lse = a.lse;
+  s.dx = a.dx;
+  s.status = status;
+  const bool grad = a.dx != nullptr;
+  note_launch();
+  return launch_pdl(a.f16 ? kernel_of<true>(D, grad) : kernel_of<false>(D, grad),
+                    dim3(static_cast<unsigned>((a.M + kTok - 1) / kTok * plan.cluster)), dim3(kThreads),
+                    static_cast<size_t>(small_smem(D, split, s.stages)), st, static_cast<unsigned>(plan.cluster), s);
+}
+
+}  // namespace qnf4

@@ -408,6 +408,50 @@ def test_loss(lib, dtype, M, V, D):
     _ok()
 
 
+# one launch, or several: either side of where one takes less time; hidden sizes around the one
+# launch's groups of 32, 64, 128, 256 and 512; tokens and entries around its 16
+LOSS_EDGES = [(15, 15, 64), (16, 16, 72), (17, 17, 88), (33, 1500, 120), (1, 31, 128), (40, 129, 136), (100, 900, 256),
+              (20, 500, 264), (50, 300, 512), (6, 170, 520), (3, 100, 1024), (700, 600, 64), (3000, 90, 80),
+              (300, 30000, 136), (7, 60000, 72), (100, 20000, 576), (1, 40000, 256), (500, 9000, 1024)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,V,D", LOSS_EDGES)
+def test_loss_in_one_launch_or_several(lib, dtype, M, V, D):
+    x, W, t = _loss_case(M, V, D, dtype, 7)
+    tt = torch.from_numpy(t).to(DEV)
+    g = _rng(12, M).random(M).astype(np.float32) + 0.5
+    loss, lse, dx = b.qlora_lm_loss(x, W, tt, grad_scale=_dev(g))
+    _check_loss(x, W, t, g.astype(np.float64), dtype, loss, lse, dx)
+    again = b.qlora_lm_loss(x, W, tt, grad_scale=_dev(g))
+    assert all(torch.equal(p, q) for p, q in zip((loss, lse, dx), again))
+    l2, e2, _ = b.qlora_lm_loss(x, W, tt, need_dx=False)
+    _check_loss(x, W, t, None, dtype, l2, e2, None)
+    _ok()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("above", [5.0, 70.0, 200.0])
+@pytest.mark.parametrize("M,V", [(600, 30000), (8, 60000), (40, 400)])
+def test_loss_spikes_in_every_form(lib, dtype, above, M, V):
+    """An entry far above the target's logit, and one far below all others."""
+    D = 64
+    rng = _rng(13, M)
+    W = rng.standard_normal((V, D)) * 0.05
+    x = rng.standard_normal((M, D))
+    W[:, 0], x[:, 0] = 0.0, 0.0
+    W[[V // 2, V - 1], 0] = 1.0
+    W[V // 3, 0] = -1.0
+    x[5, 0] = x[M // 2, 0] = x[M - 1, 0] = above
+    t = rng.integers(0, V // 4, M)
+    t[6] = -100
+    t[0], x[0, 0] = V - 1, above                  # a sure token
+    W, x = _dev(W, DT[dtype]), _dev(x, DT[dtype])
+    loss, lse, dx = b.qlora_lm_loss(x, W, torch.from_numpy(t).to(DEV))
+    _check_loss(x, W, t, None, dtype, loss, lse, dx)
+    _ok()
+
+
 @pytest.mark.parametrize("dq", [True, False])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("M,V,D", [(5, 300, 64), (140, 1025, 576)])
