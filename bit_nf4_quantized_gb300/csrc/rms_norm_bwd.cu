@@ -11,7 +11,7 @@
 // h (or one byte a value) once each: 4096 x 4096 bf16, 134 MB, 24 us, 0.82 of the measured copy
 // bandwidth (loaded by the threads: 38 us); with dweight 32 us.  Rows that are not 16-byte aligned are
 // bound by their instructions, in pairs rather than eights: 4096 x 4095, 37 us from h, 29 us from the
-// checkpoint, with dweight 42 and 33 (by single elements, loaded by the threads: 48 us).
+// checkpoint, with dweight 41 and 33 (by single elements, loaded by the threads: 48 us).
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, in
 }
 
 // dweight[k] = sum of the P groups' parts: 32 columns a CTA, 32 threads down the groups, then
-// their sums in order.
+// their sums in order.  (8 columns a CTA, on four times as many SMs, took 0 to 2 us longer.)
 __global__ void norm_dweight(const float* part, int64_t P, int64_t K, float* dweight) {
   __shared__ float red[kDwRows][kDwCols];
   pdl_allow_next();
@@ -303,8 +303,8 @@ BwdShape bwd_shape(int64_t M, int64_t K) {
   b.row = b.nv > 0 ? row_shape(C, b.nv) : RowShape{512, 1};
   // about 1024 threads an SM, each walking over rows an even number apart, so that a group's rows
   // start at the same parity (row_parity)
-  const int64_t ctas = (static_cast<int64_t>(device_sm_count()) * std::max(1, 1024 / (b.row.G * b.row.R)) + 1) / 2 * 2;
-  b.grid = static_cast<int>(std::min(ctas, (M + b.row.R - 1) / b.row.R));
+  b.grid = static_cast<int>(even_grid((M + b.row.R - 1) / b.row.R,
+                                      static_cast<int64_t>(device_sm_count()) * std::max(1, 1024 / (b.row.G * b.row.R))));
   return b;
 }
 

@@ -81,8 +81,7 @@ inline RingShape ring_shape(int64_t M, int64_t K, size_t bytes, int regs, int n)
   }
   s.smem = s.workers * s.stages * bytes + kRingPad;
   const int64_t want = (M + s.workers - 1) / s.workers;
-  const int64_t most = (static_cast<int64_t>(ctas) * device_sm_count() + 1) / 2 * 2;
-  s.grid = static_cast<unsigned>(std::min(want, most));
+  s.grid = static_cast<unsigned>(even_grid(want, static_cast<int64_t>(ctas) * device_sm_count()));
   return s;
 }
 

@@ -17,6 +17,8 @@
 // two divisions a lane.
 #pragma once
 
+#include <algorithm>
+
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -384,6 +386,14 @@ __device__ __forceinline__ float group_sum(float v, float* red, int turn) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
+}
+
+// CTAs for `want` rounds of rows where `most` are resident: as few as take no more turns each (a
+// weight gradient has a part from each), and an even number, so that all of a CTA's rows start at
+// the same parity.
+inline int64_t even_grid(int64_t want, int64_t most) {
+  const int64_t turns = std::max<int64_t>(1, (want + std::max<int64_t>(most, 1) - 1) / std::max<int64_t>(most, 1));
+  return turns == 1 ? want : ((want + turns - 1) / turns + 1) / 2 * 2;
 }
 
 // Threads of a row and rows of a CTA for C chunks with NV chunks a thread.
