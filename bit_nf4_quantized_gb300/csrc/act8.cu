@@ -33,31 +33,28 @@ struct ChunkWalk {
 
 // Four lanes to a block of 128, 32 values each (train_ops.cuh): with 8 values a lane the block's
 // reduction and divisions took longer than its bytes (4096 x 14336 bf16: 51 us; with 32, 29 us,
-// 0.91 of the measured copy bandwidth).  Rows that are not 16-byte aligned keep 8 values a lane,
-// whose narrow accesses then share sectors (4096 x 4095: 18.5 us; with 32 a lane, 45 in single elements).  Bound by
-// HBM: the activation once, one byte a value and 4 / 128 out.
-template <bool kVec>
-constexpr int quant_chunks() { return kVec ? 4 : 1; }
-template <typename T, bool kVec>
+// 0.91 of the measured copy bandwidth).  Bound by HBM: the activation once, one byte a value and
+// 4 / 128 out.
+constexpr int kQuantN = 4;
+template <typename T>
 __global__ void __launch_bounds__(kThreads) act8_quantize(const T* x, int64_t M, int64_t K, Act8View out, int* status) {
-  constexpr int kN = quant_chunks<kVec>();
   pdl_allow_next();
   pdl_wait();
-  const int64_t L = (K + kActBlock - 1) / kActBlock * (kActLanes / kN);   // lanes of a row
+  const int64_t L = (K + kActBlock - 1) / kActBlock * (kActLanes / kQuantN);   // lanes of a row
   const ChunkWalk w(static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, L);
-  const int p = kVec ? 0 : row_parity(w.m, K);
-  float v[kN][8];
+  float v[kQuantN][8];
 #pragma unroll
-  for (int u = 0; u < kN; ++u) {
-    if (w.m < M) load8<T, kVec>(x + w.m * K, chunk_of(w.c, kN, u), K, v[u], p);
+  for (int u = 0; u < kQuantN; ++u) {
+    if (w.m < M) load8<T, true>(x + w.m * K, chunk_of(w.c, kQuantN, u), K, v[u]);
     else
       for (int j = 0; j < 8; ++j) v[u][j] = 0.0f;
   }
-  const Quantized<kN> q = quantize_block<kN>(v);
-  if (w.m < M) store_block<kVec, kN>(out, w.m, w.c, K, q, status, p);
+  const Quantized<kQuantN> q = quantize_block<kQuantN>(v);
+  if (w.m < M) store_block<true, kQuantN>(out, w.m, w.c, K, q, status);
 }
 
-template <typename T, bool kVec>
+// 4096 x 14336 bf16: 27 us, 0.96 of the measured copy bandwidth.
+template <typename T>
 __global__ void __launch_bounds__(kThreads) act8_dequantize(Act8View in, int64_t M, int64_t K, const float* weight, T* out) {
   pdl_allow_next();
   pdl_wait();
@@ -68,43 +65,130 @@ __global__ void __launch_bounds__(kThreads) act8_dequantize(Act8View in, int64_t
 #pragma unroll
   for (int u = 0; u < kPer; ++u, at.next(C)) {
     const int64_t m = min(at.m, M - 1);
-    q[u] = load_codes<kVec>(in.codes + m * K, at.c, K, kVec ? 0 : row_parity(m, K));
+    q[u] = load_codes<true>(in.codes + m * K, at.c, K);
     sc[u] = in.scales[m * nb + at.c / kActLanes];
   }
 #pragma unroll
   for (int u = 0; u < kPer; ++u, w.next(C)) {
     if (w.m >= M) continue;
-    const int p = kVec ? 0 : row_parity(w.m, K);
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = code_value(q[u], j) * sc[u];
     if (weight != nullptr) {
       float g[8];
-      load_vector8<kVec>(weight, w.c, K, g, p);
+      load8<float, true>(weight, w.c, K, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= g[j];
     }
-    store8<T, kVec>(out + w.m * K, w.c, K, v, p);
+    store8<T, true>(out + w.m * K, w.c, K, v);
   }
 }
 
-template <typename T, bool kVec>
+// Rows that are not 16-byte aligned: 16 lanes take four neighbouring blocks of one row, a chunk of
+// each a lane.  Bound by instructions, most of them addresses: every access is a constant away from one
+// place, and where all four blocks end inside the row (PairQuad::whole) there are no bounds.
+// 6276 x 7046 bf16: 34 us stored, 32 read back (a chunk of any block a lane: 44 and 36);
+// 8000 x 999: 7.5 and 8.3 (10.4 and 12.7).
+struct PairQuad {
+  int64_t m, first;     // the row, the first block
+  int lane, p, at;
+  int left;             // features from the first block on, 512 at most; 0: no row
+  bool on, whole;
+  __device__ __forceinline__ PairQuad(int64_t M, int64_t K, int64_t quads)
+      : lane(threadIdx.x % kActLanes) {
+    const ChunkWalk w(static_cast<int64_t>(blockIdx.x) * (kThreads / kActLanes) + threadIdx.x / kActLanes, quads);
+    m = w.m, first = 4 * w.c, p = row_parity(w.m, K), at = 2 * lane - p;
+    on = w.m < M;
+    left = on ? static_cast<int>(min(K - first * kActBlock, static_cast<int64_t>(4 * kActBlock))) : 0;
+    whole = left == 4 * kActBlock;
+  }
+  __device__ __forceinline__ PairAt<int> block(int u) const {
+    return PairAt<int>::in(u * kActBlock, at, max(min(left - u * kActBlock, kActBlock), 0));
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) act8_quantize_pairs(const T* x, int64_t M, int64_t K, Act8View out, int* status) {
+  pdl_allow_next();
+  pdl_wait();
+  const int64_t nb = (K + kActBlock - 1) / kActBlock;
+  const PairQuad a(M, K, (nb + 3) / 4);
+  const int64_t start = a.m * K + a.first * kActBlock;
+  float v[4][8];
+  if (a.whole) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load_pairs(x + start, PairAt<int>::in(u * kActBlock, a.at, kActBlock), v[u]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load_chunk(x + start, a.block(u), v[u]);
+  }
+  float inv[4];
+  const BlockScale s = shared_scales<4>(v, threadIdx.x, inv);
+  if (!a.on) return;
+  if (a.lane % 4 == 0 && a.first + a.lane / 4 < nb) {
+    out.scales[a.m * nb + a.first + a.lane / 4] = s.scale;
+    if (s.bad) atomicCAS(status, 0, static_cast<int>(NF4_ERR_NONFINITE));
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const uint2 q = codes_of(v[u], inv[u], inv[u] < 0.0f);
+    if (a.whole) store_code_pairs(out.codes + start, PairAt<int>::in(u * kActBlock, a.at, kActBlock), q);
+    else store_code_chunk(out.codes + start, a.block(u), q);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) act8_dequantize_pairs(Act8View in, int64_t M, int64_t K, const float* weight, T* out) {
+  pdl_allow_next();
+  pdl_wait();
+  const int64_t nb = (K + kActBlock - 1) / kActBlock;
+  const PairQuad a(M, K, (nb + 3) / 4);
+  if (!a.on) return;
+  const int64_t start = a.m * K + a.first * kActBlock;
+  uint2 q[4];
+  float scale[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (a.whole) q[u] = load_code_pairs(in.codes + start, PairAt<int>::in(u * kActBlock, a.at, kActBlock));
+    else q[u] = load_code_chunk(in.codes + start, a.block(u));
+    scale[u] = in.scales[a.m * nb + min(a.first + u, nb - 1)];
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = code_value(q[u], j) * scale[u];
+    if (weight != nullptr) {
+      float g[8];
+      load_vector8<false>(weight, (a.first + u) * kActLanes + a.lane, K, g, a.p);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= g[j];
+    }
+    if (a.whole) store_pairs(out + start, PairAt<int>::in(u * kActBlock, a.at, kActBlock), v);
+    else store_chunk(out + start, a.block(u), v);
+  }
+}
+
+// Both take four chunks a thread.
+unsigned act8_ctas(int64_t M, int64_t K) {
+  static_assert(kPer == 4 && kQuantN == 4, "four chunks a thread");
+  const int64_t nb = (K + kActBlock - 1) / kActBlock;
+  const int64_t chunks = M * (K % 8 == 0 ? nb : (nb + 3) / 4 * 4) * kActLanes;
+  return static_cast<unsigned>((chunks + kThreads * kPer - 1) / (kThreads * kPer));
+}
+
+template <typename T>
 cudaError_t quantize_t(const void* x, int64_t M, int64_t K, Act8View out, int* status, cudaStream_t st) {
-  const int64_t n = M * ((K + kActBlock - 1) / kActBlock) * (kActLanes / quant_chunks<kVec>());
   note_launch();
-  return launch_pdl(act8_quantize<T, kVec>, dim3(static_cast<unsigned>((n + kThreads - 1) / kThreads)), dim3(kThreads), 0,
-                    st, 1, static_cast<const T*>(x), M, K, out, status);
+  return launch_pdl(K % 8 == 0 ? act8_quantize<T> : act8_quantize_pairs<T>, dim3(act8_ctas(M, K)), dim3(kThreads), 0, st, 1,
+                    static_cast<const T*>(x), M, K, out, status);
 }
 
 template <typename T>
 cudaError_t dequantize_t(Act8View in, int64_t M, int64_t K, const float* weight, void* out, cudaStream_t st) {
-  const int64_t n = M * ((K + kActBlock - 1) / kActBlock) * kActLanes;
-  const dim3 grid(static_cast<unsigned>((n + kThreads * kPer - 1) / (kThreads * kPer)));
   note_launch();
-  return K % 8 == 0 ? launch_pdl(act8_dequantize<T, true>, grid, dim3(kThreads), 0, st, 1, in, M, K, weight,
-                                 static_cast<T*>(out))
-                    : launch_pdl(act8_dequantize<T, false>, grid, dim3(kThreads), 0, st, 1, in, M, K, weight,
-                                 static_cast<T*>(out));
+  return launch_pdl(K % 8 == 0 ? act8_dequantize<T> : act8_dequantize_pairs<T>, dim3(act8_ctas(M, K)), dim3(kThreads), 0, st, 1,
+                    in, M, K, weight, static_cast<T*>(out));
 }
 
 // ---- dA ---------------------------------------------------------------------------------
@@ -542,15 +626,10 @@ cudaError_t launch_grad(const ActGradArgs& a, const GradPlan& g, float* part, cu
 cudaError_t launch_act8_quantize(const void* x, nf4_dtype dt, int64_t M, int64_t K, Act8View out, int* status,
                                  cudaStream_t st) {
   if (M == 0) return cudaSuccess;
-  const bool vec = K % 8 == 0;
   switch (dt) {
-    case NF4_F32:
-      return vec ? quantize_t<float, true>(x, M, K, out, status, st) : quantize_t<float, false>(x, M, K, out, status, st);
-    case NF4_BF16:
-      return vec ? quantize_t<__nv_bfloat16, true>(x, M, K, out, status, st)
-                 : quantize_t<__nv_bfloat16, false>(x, M, K, out, status, st);
-    default:
-      return vec ? quantize_t<__half, true>(x, M, K, out, status, st) : quantize_t<__half, false>(x, M, K, out, status, st);
+    case NF4_F32: return quantize_t<float>(x, M, K, out, status, st);
+    case NF4_BF16: return quantize_t<__nv_bfloat16>(x, M, K, out, status, st);
+    default: return quantize_t<__half>(x, M, K, out, status, st);
   }
 }
 

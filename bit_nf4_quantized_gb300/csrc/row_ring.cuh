@@ -148,38 +148,20 @@ __device__ __forceinline__ uint2 ring_codes(const uint8_t* row, I c, I K, int p)
   }
 }
 
-// Quantizes and stores the chunks t + u G of row m: kN = 2 or 4 blocks a half warp.  Lanes 16 / kN of
-// it come to hold one block's largest magnitude (exchanges of halves, then of whole values, for what
-// kN reductions one by one take four each), find its scale and pass it on.
+// Quantizes and stores the chunks t + u G of row m.
 template <int kN>
 __device__ __forceinline__ void store_ring_blocks(const Act8View& a, int64_t m, int64_t row, int t, int G, int K, int p,
                                                   const float (&v)[kN][8], int* status) {
-  constexpr uint32_t kAll = 0xffffffffu;
-  constexpr int kOwn = kActLanes / kN;
-  float k[kN];
-#pragma unroll
-  for (int u = 0; u < kN; ++u) k[u] = chunk_amax(v[u], 0.0f);
-#pragma unroll
-  for (int o = 8, n = kN / 2; n > 0; o /= 2, n /= 2)
-#pragma unroll
-    for (int u = 0; u < n; ++u) {
-      const float keep = t & o ? k[u + n] : k[u], give = t & o ? k[u] : k[u + n];
-      k[u] = max_abs_nan(keep, __shfl_xor_sync(kAll, give, o));
-    }
-#pragma unroll
-  for (int o = kOwn / 2; o > 0; o /= 2) k[0] = max_abs_nan(k[0], __shfl_xor_sync(kAll, k[0], o));
-  const BlockScale s(k[0]);
-  const int own = t / kActLanes + t % kActLanes / kOwn * (G / kActLanes);
-  if (t % kOwn == 0 && own * kActBlock < K) {
+  float inv[kN];
+  const BlockScale s = shared_scales<kN>(v, t, inv);
+  const int own = t / kActLanes + t % kActLanes / (kActLanes / kN) * (G / kActLanes);
+  if (t % (kActLanes / kN) == 0 && own * kActBlock < K) {
     a.scales[m * ((K + kActBlock - 1) / kActBlock) + own] = s.scale;
     if (s.bad) atomicCAS(status, 0, static_cast<int>(NF4_ERR_NONFINITE));
   }
-  const float inv = s.bad ? -1.0f : s.inv;
 #pragma unroll
-  for (int u = 0; u < kN; ++u) {
-    const float i = __shfl_sync(kAll, inv, (t & 16) + kOwn * u);
-    store_codes<false>(a.codes + row, t + u * G, K, codes_of(v[u], i, i < 0.0f), p);
-  }
+  for (int u = 0; u < kN; ++u)
+    store_codes<false>(a.codes + row, t + u * G, K, codes_of(v[u], inv[u], inv[u] < 0.0f), p);
 }
 
 }  // namespace qnf4

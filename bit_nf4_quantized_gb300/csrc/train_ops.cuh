@@ -114,6 +114,12 @@ struct PairAt {
   __device__ __forceinline__ PairAt(I c, I K, int p)
       : base((c / kActLanes) * kActBlock), at(2 * static_cast<int>(c % kActLanes) - p),
         left(static_cast<int>(max(min(K - base, static_cast<I>(kActBlock)), static_cast<I>(0)))) {}
+  PairAt() = default;
+  static __device__ __forceinline__ PairAt in(I base, int at, int left) {
+    PairAt q;
+    q.base = base, q.at = at, q.left = left;
+    return q;
+  }
   __device__ __forceinline__ int feature(int j) const {   // value j's, in the block
     return j == 0 && at < 0 ? kActBlock - 1 : at + 32 * (j / 2) + j % 2;
   }
@@ -164,6 +170,17 @@ __device__ __forceinline__ void load_pairs(const T* row, const PairAt<I>& q, flo
   if (q.at < 0) v[0] = Elem<T>::to(last);
 }
 
+// The same of any block: zeros past the row's end.
+template <typename T, typename I>
+__device__ __forceinline__ void load_chunk(const T* row, const PairAt<I>& q, float (&v)[8]) {
+  if (q.left == kActBlock) {
+    load_pairs(row, q, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = q.feature(j) < q.left ? Elem<T>::to(row[q.base + q.feature(j)]) : 0.0f;
+  }
+}
+
 // The 8 values of chunk c (16 chunks a block) of a row of K: zeros past the row's end.  p: parity
 // of the row's start (row_parity; kVec: unused).
 template <typename T, bool kVec, typename I>
@@ -181,16 +198,33 @@ __device__ __forceinline__ void load8(const T* row, I c, I K, float (&v)[8], int
       for (int j = 0; j < 8; ++j) v[j] = 0.0f;
     }
   } else {
-    const PairAt<I> q(c, K, p);
-    if (q.left == kActBlock) {
-      load_pairs(row, q, v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = q.feature(j) < q.left ? Elem<T>::to(row[q.base + q.feature(j)]) : 0.0f;
-    }
+    load_chunk(row, PairAt<I>(c, K, p), v);
   }
 }
 
+template <typename T, typename I>
+__device__ __forceinline__ void store_pairs(T* row, const PairAt<I>& q, const float (&v)[8]) {
+  using Word = typename Pair<T>::Word;
+  Word* dst = reinterpret_cast<Word*>(row + q.base + q.at);
+#pragma unroll
+  for (int u = 1; u < 4; ++u) dst[16 * u] = pack2(v[2 * u], v[2 * u + 1], T{});
+  if (q.at < 0) {
+    row[q.base + kActBlock - 1] = Elem<T>::from(v[0]);
+    row[q.base] = Elem<T>::from(v[1]);
+  } else {
+    dst[0] = pack2(v[0], v[1], T{});
+  }
+}
+template <typename T, typename I>
+__device__ __forceinline__ void store_chunk(T* row, const PairAt<I>& q, const float (&v)[8]) {
+  if (q.left == kActBlock) {
+    store_pairs(row, q, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (q.feature(j) < q.left) row[q.base + q.feature(j)] = Elem<T>::from(v[j]);
+  }
+}
 template <typename T, bool kVec, typename I>
 __device__ __forceinline__ void store8(T* row, I c, I K, const float (&v)[8], int p = 0) {
   if constexpr (kVec) {
@@ -203,23 +237,7 @@ __device__ __forceinline__ void store8(T* row, I c, I K, const float (&v)[8], in
       if (sizeof(T) == 4) dst[1] = *reinterpret_cast<uint4*>(raw + 4);
     }
   } else {
-    const PairAt<I> q(c, K, p);
-    if (q.left == kActBlock) {
-      using Word = typename Pair<T>::Word;
-      Word* dst = reinterpret_cast<Word*>(row + q.base + q.at);
-#pragma unroll
-      for (int u = 1; u < 4; ++u) dst[16 * u] = pack2(v[2 * u], v[2 * u + 1], T{});
-      if (q.at < 0) {
-        row[q.base + kActBlock - 1] = Elem<T>::from(v[0]);
-        row[q.base] = Elem<T>::from(v[1]);
-      } else {
-        dst[0] = pack2(v[0], v[1], T{});
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (q.feature(j) < q.left) row[q.base + q.feature(j)] = Elem<T>::from(v[j]);
-    }
+    store_chunk(row, PairAt<I>(c, K, p), v);
   }
 }
 
@@ -243,6 +261,19 @@ __device__ __forceinline__ uint2 load_code_pairs(const int8_t* row, const PairAt
   return q;
 }
 
+template <typename I>
+__device__ __forceinline__ uint2 load_code_chunk(const int8_t* row, const PairAt<I>& f) {
+  if (f.left == kActBlock) return load_code_pairs(row, f);
+  uint2 q = make_uint2(0, 0);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t b = f.feature(j) < f.left ? static_cast<uint8_t>(row[f.base + f.feature(j)]) : 0u;
+    if (j < 4) q.x |= b << (8 * j);
+    else q.y |= b << (8 * (j - 4));
+  }
+  return q;
+}
+
 // A lane's 8 codes, packed in order (byte j: value j).
 template <bool kVec, typename I>
 __device__ __forceinline__ uint2 load_codes(const int8_t* row, I c, I K, int p = 0) {
@@ -250,17 +281,7 @@ __device__ __forceinline__ uint2 load_codes(const int8_t* row, I c, I K, int p =
   if constexpr (kVec) {
     if (c * 8 < K) q = *reinterpret_cast<const uint2*>(row + c * 8);
   } else {
-    const PairAt<I> f(c, K, p);
-    if (f.left == kActBlock) {
-      q = load_code_pairs(row, f);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t b = f.feature(j) < f.left ? static_cast<uint8_t>(row[f.base + f.feature(j)]) : 0u;
-        if (j < 4) q.x |= b << (8 * j);
-        else q.y |= b << (8 * (j - 4));
-      }
-    }
+    q = load_code_chunk(row, PairAt<I>(c, K, p));
   }
   return q;
 }
@@ -332,29 +353,65 @@ __device__ __forceinline__ Quantized<kN> quantize_block(const float (&v)[kN][8])
   return q;
 }
 
+// The scales of kN = 2 or 4 blocks that a half warp holds, one chunk of each a lane (v[u]: of block u).
+// Lanes 16 / kN of it come to hold one block's largest magnitude (exchanges of halves, then of
+// whole values, for what kN reductions one by one take four each), find its scale, which is
+// returned, and pass its inverse on (-1: not finite).  Every lane of the warp calls it.
+template <int kN>
+__device__ __forceinline__ BlockScale shared_scales(const float (&v)[kN][8], int t, float (&inv)[kN]) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  constexpr int kOwn = kActLanes / kN;
+  float k[kN];
+#pragma unroll
+  for (int u = 0; u < kN; ++u) k[u] = chunk_amax(v[u], 0.0f);
+#pragma unroll
+  for (int o = 8, n = kN / 2; n > 0; o /= 2, n /= 2)
+#pragma unroll
+    for (int u = 0; u < n; ++u) {
+      const float keep = t & o ? k[u + n] : k[u], give = t & o ? k[u] : k[u + n];
+      k[u] = max_abs_nan(keep, __shfl_xor_sync(kAll, give, o));
+    }
+#pragma unroll
+  for (int o = kOwn / 2; o > 0; o /= 2) k[0] = max_abs_nan(k[0], __shfl_xor_sync(kAll, k[0], o));
+  const BlockScale s(k[0]);
+  const float own = s.bad ? -1.0f : s.inv;
+#pragma unroll
+  for (int u = 0; u < kN; ++u) inv[u] = __shfl_sync(kAll, own, (t & 16) + kOwn * u);
+  return s;
+}
+
+template <typename I>
+__device__ __forceinline__ void store_code_pairs(int8_t* row, const PairAt<I>& f, uint2 q) {
+  uint16_t* dst = reinterpret_cast<uint16_t*>(row + f.base + f.at);
+  dst[16] = static_cast<uint16_t>(q.x >> 16);
+  dst[32] = static_cast<uint16_t>(q.y);
+  dst[48] = static_cast<uint16_t>(q.y >> 16);
+  if (f.at < 0) {
+    row[f.base + kActBlock - 1] = static_cast<int8_t>(q.x);
+    row[f.base] = static_cast<int8_t>(q.x >> 8);
+  } else {
+    dst[0] = static_cast<uint16_t>(q.x);
+  }
+}
+
+template <typename I>
+__device__ __forceinline__ void store_code_chunk(int8_t* row, const PairAt<I>& f, uint2 q) {
+  if (f.left == kActBlock) {
+    store_code_pairs(row, f, q);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (f.feature(j) < f.left) row[f.base + f.feature(j)] = static_cast<int8_t>((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+  }
+}
+
 // Stores chunk c's codes.
 template <bool kVec, typename I>
 __device__ __forceinline__ void store_codes(int8_t* row, I c, I K, uint2 q, int p) {
   if constexpr (kVec) {
     if (c * 8 < K) *reinterpret_cast<uint2*>(row + c * 8) = q;
   } else {
-    const PairAt<I> f(c, K, p);
-    if (f.left == kActBlock) {
-      uint16_t* dst = reinterpret_cast<uint16_t*>(row + f.base + f.at);
-      dst[16] = static_cast<uint16_t>(q.x >> 16);
-      dst[32] = static_cast<uint16_t>(q.y);
-      dst[48] = static_cast<uint16_t>(q.y >> 16);
-      if (f.at < 0) {
-        row[f.base + kActBlock - 1] = static_cast<int8_t>(q.x);
-        row[f.base] = static_cast<int8_t>(q.x >> 8);
-      } else {
-        dst[0] = static_cast<uint16_t>(q.x);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (f.feature(j) < f.left) row[f.base + f.feature(j)] = static_cast<int8_t>((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
-    }
+    store_code_chunk(row, PairAt<I>(c, K, p), q);
   }
 }
 
