@@ -10,11 +10,10 @@
 // those too long for it are loaded by the threads themselves.  Bound by HBM: dy, dresidual, dx and
 // h (or one byte a value) once each: 4096 x 4096 bf16, 134 MB, 24 us, 0.82 of the measured copy
 // bandwidth (loaded by the threads: 38 us); with dweight 32 us.  Rows that are not 16-byte aligned are
-// bound by their instructions, in pairs rather than eights: 4096 x 4095, 37 us from h, 29 us from the
-// checkpoint, with dweight 41 and 33 (by single elements, loaded by the threads: 48 us).
+// bound by their instructions, in pairs rather than eights: 4096 x 4095, 30 us from h, 31 us from the
+// checkpoint, with dweight 36 (by single elements, loaded by the threads: 48 us).
 #include <algorithm>
 #include <mutex>
-#include <type_traits>
 
 #include "row_ring.cuh"
 
@@ -164,7 +163,7 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, in
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (blockDim.x / G) + w;
   const int64_t nb = (a.K + kActBlock - 1) / kActBlock;
   constexpr int kScales = kVec ? 1 : kN;             // blocks that a thread's chunks belong to
-  auto block = [&](int u) { return min(static_cast<int64_t>(ring_chunk<kVec, kN>(t, G, u) / kActLanes), nb - 1); };
+  auto block = [&](int u) { return min(static_cast<int64_t>(ring_chunk<kVec, kN>(t, u) / kActLanes), nb - 1); };
   const float invK = 1.0f / static_cast<float>(a.K);
   const int p = kVec ? 0 : row_parity(first, a.K);
   auto issue = [&](int64_t m, int s) {
@@ -190,7 +189,7 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, in
   float dw[kN][8], held[kHoldW ? kN : 1][8];
 #pragma unroll
   for (int u = 0; u < kN; ++u) {
-    if (kHoldW) load_vector8<kVec, int64_t>(a.weight, ring_chunk<kVec, kN>(t, G, u), a.K, held[kHoldW ? u : 0], p);
+    if (kHoldW) load_vector8<kVec>(a.weight, ring_chunk<kVec, kN>(t, u), a.K, held[kHoldW ? u : 0], p);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[u][j] = 0.0f;
   }
@@ -202,7 +201,11 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, in
   int s = 0, turn = 0;
   uint32_t ph = 0;
   for (int64_t m = first; m < a.M; m += workers, turn ^= 1) {
-    const std::conditional_t<kVec, int64_t, int> K = kVec ? a.K : not_kept(a.K);
+    const RingPairs<kN> pairs(t, kVec ? 0 : not_kept(a.K), p);
+    auto get = [&](const uint8_t* row, int u, float (&v)[8]) {
+      if constexpr (kVec) load8<T, true>(reinterpret_cast<const T*>(row), chunk_of(t, kN, u), a.K, v);
+      else pairs.template load<T>(row, u, v);
+    };
     const float rstd = rstd_next;
     float scale[kScales];
 #pragma unroll
@@ -221,16 +224,17 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, in
     float sum = 0.0f;
 #pragma unroll
     for (int u = 0; u < kN; ++u) {
-      const auto c = ring_chunk<kVec, kN>(t, G, u);
       float wt[8];
-      if (!kHoldW) load_vector8<kVec>(a.weight, c, K, wt, p);
-      ring8<T, kVec>(stage, c, K, g[u], p);
+      if (!kHoldW) load_vector8<kVec>(a.weight, ring_chunk<kVec, kN>(t, u), a.K, wt, p);
+      get(stage, u, g[u]);
       if (kCk) {
-        const uint2 q = ring_codes<kVec>(saved, c, K, p);
+        uint2 q;
+        if constexpr (kVec) q = load_codes<true>(reinterpret_cast<const int8_t*>(saved), chunk_of(t, kN, u), a.K);
+        else q = pairs.load_codes(saved, u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) n[u][j] = code_value(q, j) * scale[kVec ? 0 : u];
       } else {
-        ring8<T, kVec>(saved, c, K, n[u], p);
+        get(saved, u, n[u]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) n[u][j] *= rstd;
       }
@@ -244,15 +248,16 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, in
     const float mean = worker_sum(sum, G, red, turn) * invK;
 #pragma unroll
     for (int u = 0; u < kN; ++u) {
-      const auto c = ring_chunk<kVec, kN>(t, G, u);
       float o[8];
-      if (a.dresidual != nullptr) ring8<T, kVec>(stage + slot + saved_slot, c, K, o, p);
+      if (a.dresidual != nullptr) get(stage + slot + saved_slot, u, o);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float d = rstd * (g[u][j] - n[u][j] * mean);
         o[j] = a.dresidual != nullptr ? d + o[j] : d;
       }
-      store8<T, kVec>(static_cast<T*>(a.dx) + m * a.K, c, K, o, p);
+      T* dx = static_cast<T*>(a.dx) + m * a.K;
+      if constexpr (kVec) store8<T, true>(dx, chunk_of(t, kN, u), a.K, o);
+      else pairs.store(dx, u, o);
     }
     if (G == 32) __syncwarp();
     else __syncthreads();
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_ring(const NormBwdArgs a, in
   if (kDw) {
     float* part = a.partial + first * a.K;
 #pragma unroll
-    for (int u = 0; u < kN; ++u) store8<float, kVec, int64_t>(part, ring_chunk<kVec, kN>(t, G, u), a.K, dw[u], p);
+    for (int u = 0; u < kN; ++u) store8<float, kVec>(part, ring_chunk<kVec, kN>(t, u), a.K, dw[u], p);
   }
 }
 

@@ -8,10 +8,9 @@
 // sum.  Rows come through a ring of bulk copies (row_ring.cuh); those too long for it, and short
 // ones that are not 16-byte aligned, are loaded by the threads themselves.  4096 x 4096 bf16 with
 // residual and checkpoint, 152 MB: 26 us, 0.86 of the measured copy bandwidth (loaded by the
-// threads: 37 us).  4096 x 4095, bound by its instructions: 42 us (by single elements: 61 us).
+// threads: 37 us).  4096 x 4095, bound by its instructions: 39 us (by single elements: 61 us).
 #include <algorithm>
 #include <mutex>
-#include <type_traits>
 
 #include "row_ring.cuh"
 
@@ -21,7 +20,7 @@ namespace {
 // A thread's registers with two chunks in pairs: three CTAs of 256 threads an SM.
 constexpr int kPairRegs = 80;
 // Rows of pairs up to this length are loaded by their threads (4096 x 577: 10 us, by the ring 12;
-// 777 x 1531: 6.3 both; 4096 x 4095: 49 and 42).
+// 777 x 1531: 6.3 and 5.9; 4096 x 4095: 49 and 39).
 constexpr int64_t kPairDirectK = 1024;
 
 // kNv = 0: rows longer than the registers of a CTA hold; the row is read twice.
@@ -138,11 +137,19 @@ __global__ void __maxnreg__(kN == 2 ? kPairRegs : 128) rms_norm_fwd_ring(const N
     for (int s = 0; s < stages; ++s) issue(first + s * workers, s);
   float wt[kN][8];      // the thread's columns are the same for every row
 #pragma unroll
-  for (int u = 0; u < kN; ++u) load_vector8<kVec, int64_t>(a.weight, ring_chunk<kVec, kN>(t, G, u), a.K, wt[u], p);
+  for (int u = 0; u < kN; ++u) load_vector8<kVec>(a.weight, ring_chunk<kVec, kN>(t, u), a.K, wt[u], p);
   int s = 0, turn = 0;
   uint32_t ph = 0;
   for (int64_t m = first; m < a.M; m += workers, turn ^= 1) {
-    const std::conditional_t<kVec, int64_t, int> K = kVec ? a.K : not_kept(a.K);
+    const RingPairs<kN> pairs(t, kVec ? 0 : not_kept(a.K), p);
+    auto get = [&](const uint8_t* row, int u, float (&v)[8]) {
+      if constexpr (kVec) load8<T, true>(reinterpret_cast<const T*>(row), chunk_of(t, kN, u), a.K, v);
+      else pairs.template load<T>(row, u, v);
+    };
+    auto put = [&](T* row, int u, const float (&v)[8]) {
+      if constexpr (kVec) store8<T, true>(row, chunk_of(t, kN, u), a.K, v);
+      else pairs.store(row, u, v);
+    };
     // a wait that gives up leaves the loop's shape as it is: the later ones return at once
     tc::mbar_wait(bar_at + 8 * s, ph, &gave_up, status);
     const uint8_t* stage = ring + s * bytes + (kVec ? 0 : row_shift(m, row_bytes));
@@ -150,11 +157,10 @@ __global__ void __maxnreg__(kN == 2 ? kPairRegs : 128) rms_norm_fwd_ring(const N
     float ss = 0.0f;
 #pragma unroll
     for (int u = 0; u < kN; ++u) {
-      const auto c = ring_chunk<kVec, kN>(t, G, u);
-      ring8<T, kVec>(stage, c, K, h[u], p);
+      get(stage, u, h[u]);
       if (a.residual != nullptr) {
         float r[8];
-        ring8<T, kVec>(stage + slot, c, K, r, p);
+        get(stage + slot, u, r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[u][j] += r[j];
       }
@@ -168,19 +174,18 @@ __global__ void __maxnreg__(kN == 2 ? kPairRegs : 128) rms_norm_fwd_ring(const N
     const int64_t at = m * a.K;
 #pragma unroll
     for (int u = 0; u < kN; ++u) {
-      const auto c = ring_chunk<kVec, kN>(t, G, u);
-      if (a.h != nullptr) store8<T, kVec>(static_cast<T*>(a.h) + at, c, K, h[u], p);
+      if (a.h != nullptr) put(static_cast<T*>(a.h) + at, u, h[u]);
       float y[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[u][j] *= rstd, y[j] = h[u][j] * wt[u][j];
-      store8<T, kVec>(static_cast<T*>(a.y) + at, c, K, y, p);
+      put(static_cast<T*>(a.y) + at, u, y);
     }
     if (a.act.codes != nullptr) {
       if constexpr (kVec) {
         const Quantized<kN> q = quantize_block<kN>(h);
-        store_block<true, kN>(a.act, m, t, K, q, status);
+        store_block<true, kN>(a.act, m, t, a.K, q, status);
       } else {
-        store_ring_blocks<kN>(a.act, m, at, t, G, K, p, h, status);
+        store_ring_blocks<kN>(a.act, m, at, t, static_cast<int>(a.K), pairs, h, status);
       }
     }
     if (++s == stages) s = 0, ph ^= 1u;

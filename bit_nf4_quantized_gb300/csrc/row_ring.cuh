@@ -66,7 +66,8 @@ struct RingShape {
 };
 inline RingShape ring_shape(int64_t M, int64_t K, size_t bytes, int regs, int n) {
   RingShape s{};
-  const int64_t lanes = (K + kActBlock - 1) / kActBlock * (kActLanes / n);
+  const int64_t blocks = (K + kActBlock - 1) / kActBlock;
+  const int64_t lanes = K % 8 == 0 ? blocks * (kActLanes / n) : (blocks + n - 1) / n * kActLanes;
   if (lanes < 16 || lanes > 512) return s;   // under half a warp busy, or over the registers
   s.G = static_cast<int>((lanes + 31) / 32 * 32);
   s.workers = s.G == 32 ? kRingWarpWorkers : 1;
@@ -106,62 +107,74 @@ __device__ __forceinline__ int not_kept(int64_t K) {
   return k;
 }
 
-// Chunk u of a worker's thread t: a block's chunks lie in a thread (kVec), or side by side in 16
-// threads, whose pairs are then next to each other.
+// Chunk u of a worker's thread t: kN chunks of one block (kVec), or one of each of kN neighbouring
+// blocks, whose pairs are then next to the neighbouring threads'.
 template <bool kVec, int kN>
-__device__ __forceinline__ auto ring_chunk(int t, int G, int u) {
+__device__ __forceinline__ int64_t ring_chunk(int t, int u) {
   if constexpr (kVec) return chunk_of(t, kN, u);
-  else return t + u * G;
+  else return (t / kActLanes * kN + u) * kActLanes + t % kActLanes;
 }
 
-// 8 values of chunk c from a row in shared memory (zeros past the row's end).
-template <typename T, bool kVec, typename I>
-__device__ __forceinline__ void ring8(const uint8_t* row, I c, I K, float (&v)[8], int p) {
-  const T* r = reinterpret_cast<const T*>(row);
-  if constexpr (kVec) {
-    load8<T, true>(r, c, K, v);
-  } else {
-    const PairAt<I> q(c, K, p);
-    if (q.left > 0) load_pairs(r, q, v);
-    if (q.left < kActBlock) {
+// A thread's pairs: everything is a constant away from `base`, the first of its kN blocks.
+template <int kN>
+struct RingPairs {
+  int base, at, left;
+  bool whole;           // all kN blocks end inside the row
+  __device__ __forceinline__ RingPairs(int t, int K, int p)
+      : base(t / kActLanes * kN * kActBlock), at(2 * (t % kActLanes) - p), left(max(min(K - base, kN * kActBlock), 0)),
+        whole(left == kN * kActBlock) {}
+  __device__ __forceinline__ PairAt<int> full(int u) const { return PairAt<int>::in(u * kActBlock, at, kActBlock); }
+  __device__ __forceinline__ PairAt<int> block(int u) const {
+    return PairAt<int>::in(u * kActBlock, at, max(min(left - u * kActBlock, kActBlock), 0));
+  }
+  // chunk u of a row in shared memory (zeros past the row's end)
+  template <typename T>
+  __device__ __forceinline__ void load(const uint8_t* row, int u, float (&v)[8]) const {
+    const T* r = reinterpret_cast<const T*>(row) + base;
+    if (whole) {
+      load_pairs(r, full(u), v);
+    } else {
+      const PairAt<int> q = block(u);
+      if (q.left > 0) load_pairs(r, q, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = q.feature(j) < q.left ? v[j] : 0.0f;
     }
   }
-}
-
-// 8 codes of chunk c (zeros past the row's end).
-template <bool kVec, typename I>
-__device__ __forceinline__ uint2 ring_codes(const uint8_t* row, I c, I K, int p) {
-  const int8_t* r = reinterpret_cast<const int8_t*>(row);
-  if constexpr (kVec) {
-    return load_codes<true>(r, c, K);
-  } else {
-    const PairAt<I> q(c, K, p);
+  __device__ __forceinline__ uint2 load_codes(const uint8_t* row, int u) const {
+    const int8_t* r = reinterpret_cast<const int8_t*>(row) + base;
+    if (whole) return load_code_pairs(r, full(u));
+    const PairAt<int> q = block(u);
     uint2 w = q.left > 0 ? load_code_pairs(r, q) : make_uint2(0, 0);
-    if (q.left < kActBlock) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (q.feature(j) >= q.left) (j < 4 ? w.x : w.y) &= ~(0xffu << (8 * (j & 3)));
-    }
+    for (int j = 0; j < 8; ++j)
+      if (q.feature(j) >= q.left) (j < 4 ? w.x : w.y) &= ~(0xffu << (8 * (j & 3)));
     return w;
   }
-}
+  // to a row in global memory
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, int u, const float (&v)[8]) const {
+    if (whole) store_pairs(row + base, full(u), v);
+    else store_chunk(row + base, block(u), v);
+  }
+  __device__ __forceinline__ void store_codes(int8_t* row, int u, uint2 q) const {
+    if (whole) store_code_pairs(row + base, full(u), q);
+    else store_code_chunk(row + base, block(u), q);
+  }
+};
 
-// Quantizes and stores the chunks t + u G of row m.
+// Quantizes and stores a thread's pairs of row m, which starts at element `row`.
 template <int kN>
-__device__ __forceinline__ void store_ring_blocks(const Act8View& a, int64_t m, int64_t row, int t, int G, int K, int p,
+__device__ __forceinline__ void store_ring_blocks(const Act8View& a, int64_t m, int64_t row, int t, int K, const RingPairs<kN>& at,
                                                   const float (&v)[kN][8], int* status) {
   float inv[kN];
   const BlockScale s = shared_scales<kN>(v, t, inv);
-  const int own = t / kActLanes + t % kActLanes / (kActLanes / kN) * (G / kActLanes);
+  const int own = t / kActLanes * kN + t % kActLanes / (kActLanes / kN);
   if (t % (kActLanes / kN) == 0 && own * kActBlock < K) {
     a.scales[m * ((K + kActBlock - 1) / kActBlock) + own] = s.scale;
     if (s.bad) atomicCAS(status, 0, static_cast<int>(NF4_ERR_NONFINITE));
   }
 #pragma unroll
-  for (int u = 0; u < kN; ++u)
-    store_codes<false>(a.codes + row, t + u * G, K, codes_of(v[u], inv[u], inv[u] < 0.0f), p);
+  for (int u = 0; u < kN; ++u) at.store_codes(a.codes + row, u, codes_of(v[u], inv[u], inv[u] < 0.0f));
 }
 
 }  // namespace qnf4
