@@ -888,7 +888,8 @@ cudaError_t launch_lm_gemm(const LmParams& p, const CUtensorMap& a, const CUtens
 }  // namespace
 
 size_t lm_loss_ws_bytes(int64_t M, int64_t V, int64_t D, bool stored, bool grad) {
-  if (lm_small_plan(M, V, D, grad).cluster > 0) return a1024(stored ? 2 * static_cast<size_t>(V) * D : 1);
+  const LmSmallPlan small = lm_small_plan(M, V, D, grad);
+  if (small.cluster > 0) return a1024(lm_small_ws_bytes(M, D, small)) + a1024(stored ? 2 * static_cast<size_t>(V) * D : 1);
   return LmLayout(M, V, D, stored, grad).total;
 }
 
@@ -897,8 +898,9 @@ cudaError_t lm_loss(const LmLossArgs& a, void* ws, int* status, cudaStream_t st)
   const LmSmallPlan small = lm_small_plan(a.M, a.V, a.D, grad);
   if (small.cluster > 0) {
     cudaError_t e = cudaSuccess;
-    if (stored) e = launch_dequantize(a.W, ws, a.f16 ? NF4_F16 : NF4_BF16, st);
-    return e != cudaSuccess ? e : launch_lm_small(a, small, stored ? ws : a.w16, status, st);
+    char* wb = static_cast<char*>(ws) + a1024(lm_small_ws_bytes(a.M, a.D, small));
+    if (stored) e = launch_dequantize(a.W, wb, a.f16 ? NF4_F16 : NF4_BF16, st);
+    return e != cudaSuccess ? e : launch_lm_small(a, small, stored ? wb : a.w16, ws, status, st);
   }
   const LmLayout L(a.M, a.V, a.D, stored, grad);
   char* w = static_cast<char*>(ws);

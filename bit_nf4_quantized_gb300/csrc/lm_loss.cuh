@@ -44,14 +44,17 @@ struct LmStreamArgs {
 int lm_stream_ctas();
 cudaError_t launch_lm_stream(const LmStreamArgs& a, bool scores, bool f16, cudaStream_t st);
 
-// lm_small.cu: everything in one launch, for few products.  cluster = 0: lm_loss.cu's launches take
-// less time.
-constexpr int64_t kSmallMaxD = 1024;
+// lm_small.cu: everything in one pass, for few products or few tokens.  cluster = 0: lm_loss.cu's
+// launches take less time.
+constexpr int64_t kSmallMaxD = 2048;
 struct LmSmallPlan {
   int cluster;              // CTAs that share 16 tokens
+  bool parts;               // their sums are joined by a second launch
 };
 LmSmallPlan lm_small_plan(int64_t M, int64_t V, int64_t D, bool grad);
-cudaError_t launch_lm_small(const LmLossArgs& a, const LmSmallPlan& plan, const void* W, int* status, cudaStream_t st);
+size_t lm_small_ws_bytes(int64_t M, int64_t D, const LmSmallPlan& plan);
+cudaError_t launch_lm_small(const LmLossArgs& a, const LmSmallPlan& plan, const void* W, void* ws, int* status,
+                            cudaStream_t st);
 
 // stored: the head is given as NF4; grad: dx is asked for.
 size_t lm_loss_ws_bytes(int64_t M, int64_t V, int64_t D, bool stored, bool grad);

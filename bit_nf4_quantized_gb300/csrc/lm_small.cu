@@ -1,18 +1,19 @@
-// The loss and its gradient in one launch, for few products.
+// The loss and its gradient in one pass, for few products or few tokens.
 //
-// lm_loss.cu's launches follow one another (preparation, scores, their repetition, gradient, totals),
-// and at small sizes their latencies are all its time.  Here a cluster of CTAs takes 16 tokens and
-// the whole vocabulary, each CTA a part of it, each of its groups of warps 16 entries at a time:
-// z = x W^T (m16n8k16 products, operands by ldmatrix, W's rows by bulk copies), the group's running
-// maximum m of each token, p = exp(z - m) in 16 bits, acc = acc exp(m_old - m) + p W with the same rows.
-// A warp's z is in the lanes where p is wanted, so groups share nothing until they add their sums,
-// in the CTA and then through the cluster's distributed shared memory, and finish the tokens as
-// lm_finish does.  The mathematics is lm_loss.cu's with m for the reference R: p is at most 1, so no part
-// is ever repeated, and a target's logit is taken as its group meets it.
+// lm_loss.cu's launches follow one another (preparation, scores, their repetition, gradient, totals):
+// at small sizes their latencies are all its time, and with few tokens its tiles of 256 are almost
+// empty and read W twice.  Here a number of CTAs share 16 tokens, each taking a part of the vocabulary,
+// each of its groups of warps 16 entries at a time: z = x W^T (m16n8k16 products, operands by
+// ldmatrix, W's rows by bulk copies), the group's running maximum m of each token, p = exp(z - m) in 16
+// bits, acc = acc exp(m_old - m) + p W with the same rows.  A warp's z is in the lanes where p is wanted,
+// so groups share nothing until they add their sums, in the CTA and then
+//   a cluster: through its distributed shared memory, finishing the tokens as lm_finish does; or
+//   parts: with few tokens all SMs take part, and lm_small_finish joins what they leave in the workspace.
+// The mathematics is lm_loss.cu's with m for the reference R: p is at most 1, so no part is ever
+// repeated, and a target's logit is taken as its group meets it.
 //
 // Bound by latency at its smallest, then by what an SM takes in: every CTA reads its part of W for
-// 16 tokens only (8 rows of 512 bytes in 90 ns: a row's copy costs 5 ns and its bytes at 90 GB/s), which
-// limits it to few products (lm_small_plan).
+// 16 tokens only (a row's copy costs about 5 ns and its bytes at 90 GB/s).
 #include <algorithm>
 #include <mutex>
 
@@ -32,6 +33,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kStagesMax = 4;
 constexpr int kWarpD = 256;           // features a warp sums at most
 constexpr int kClusterMax = 8;
+constexpr int kPartsMax = kThreads;   // of a vocabulary that the whole device shares
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct SmallArgs {
@@ -45,6 +47,8 @@ struct SmallArgs {
   float* loss;
   float* lse;
   void* dx;
+  float* part_stat;   // [3][parts][tokens]: largest logit, sum, target's logit; nullptr: a cluster finishes the tokens
+  float* part_acc;    // [parts][tokens][D]
   int* status;
 };
 
@@ -88,9 +92,8 @@ __device__ __forceinline__ float2 unpack16(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// A group of kSplit warps takes steps of 16 entries; each of its warps computes their logits and
-// then sums its 8 kNt features (kNt = 0: no gradient).  A warp's logits are the fragments of its
-// gradient's products, so groups share nothing before the end.
+// A group of kSplit warps takes steps of 16 entries; each of its warps computes their logits' sums over
+// its 256 features, which the group adds, and then its 8 kNt features of the gradient (kNt = 0: none).
 template <bool F16, int kNt, int kSplit>
 __global__ void __launch_bounds__(kThreads, kNt == 8 ? 2 : 1) lm_small(const SmallArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -101,6 +104,7 @@ __global__ void __launch_bounds__(kThreads, kNt == 8 ? 2 : 1) lm_small(const Sma
   __shared__ float factor[kGroups > kClusterMax ? kGroups : kClusterMax][kTok];
   __shared__ float2 coef[kTok];
   __shared__ uint64_t bars[kGroups][kStagesMax], x_bar;
+  __shared__ float exchange[kSplit > 1 ? kWarps : 1][8][32];
   __shared__ int gave_up;
   const int thread = threadIdx.x, warp = thread >> 5, lane = thread & 31, g = lane >> 2, c = lane & 3;
   const int group = warp / kSplit, part = warp % kSplit, in_group = thread % kGroupThreads;
@@ -175,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, kNt == 8 ? 2 : 1) lm_small(const Sma
   __syncthreads();              // the zeros are there
   tc::mbar_wait(tc::smem_u32(&x_bar), 0, &gave_up, a.status);
 
+  const int k_first = part * (kWarpD / 32), k_last = kSplit == 1 ? pairs : min(pairs, k_first + kWarpD / 32);
   int stage = 0;
   uint32_t phase = 0;
   for (int step = first; step < last; step += kGroups) {
@@ -182,19 +187,39 @@ __global__ void __launch_bounds__(kThreads, kNt == 8 ? 2 : 1) lm_small(const Sma
     tc::mbar_wait(bar + 8 * stage, phase, &gave_up, a.status);
     const uint32_t w = wbuf + stage * step_bytes;
     float z[4][2][4] = {};        // [product modulo 4][entries 0-7 or 8-15]: short chains
-    for (int k = 0; k < pairs; k += 2) {
+    for (int k = k_first; k < k_last; k += 2) {
       uint32_t b[4][4], p[4][4];
 #pragma unroll
       for (int h = 0; h < 4; ++h)
-        if (h < 2 || k + 1 < pairs) {
+        if (h < 2 || k + 1 < k_last) {
           ldmatrix4(b[h], w + z_at + 64 * k + 32 * h);
           ldmatrix4(p[h], x_at + 64 * k + 32 * h);
         }
 #pragma unroll
       for (int h = 0; h < 4; ++h)
-        if (h < 2 || k + 1 < pairs) {
+        if (h < 2 || k + 1 < k_last) {
           mma16816<F16>(z[h][0], p[h][0], p[h][1], p[h][2], p[h][3], b[h][0], b[h][1]);
           mma16816<F16>(z[h][1], p[h][0], p[h][1], p[h][2], p[h][3], b[h][2], b[h][3]);
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[0][h][q] = (z[0][h][q] + z[1][h][q]) + (z[2][h][q] + z[3][h][q]);
+    if (kSplit > 1) {             // the group's warps add their parts of the contraction, in order
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) exchange[kSplit > 1 ? warp : 0][4 * h + q][lane] = z[0][h][q];
+      group_sync();
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int y = 0; y < kSplit; ++y) sum += exchange[kSplit > 1 ? group * kSplit + y : 0][4 * h + q][lane];
+          z[0][h][q] = sum;
         }
     }
     const int v = step * kRows + 2 * c;    // this lane's entries v, v + 1, v + 8, v + 9 of tokens g, g + 8
@@ -203,7 +228,6 @@ __global__ void __launch_bounds__(kThreads, kNt == 8 ? 2 : 1) lm_small(const Sma
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        z[0][h][q] = (z[0][h][q] + z[1][h][q]) + (z[2][h][q] + z[3][h][q]);
         if (v + 8 * h + (q & 1) < a.V) (q < 2 ? n0 : n1) = fmaxf(q < 2 ? n0 : n1, z[0][h][q] * kLog2e);
       }
 #pragma unroll
@@ -312,6 +336,23 @@ __global__ void __launch_bounds__(kThreads, kNt == 8 ? 2 : 1) lm_small(const Sma
       *reinterpret_cast<float4*>(sums + 4 * i) = s;
     }
   }
+  if (a.part_stat != nullptr) {
+    __syncthreads();
+    const int64_t tokens = static_cast<int64_t>(gridDim.x) / C * kTok, at = rank * tokens + t0;
+    if (thread < kTok) {
+      a.part_stat[at + thread] = tok_max[thread];
+      a.part_stat[C * tokens + at + thread] = tok_sum[thread];
+      a.part_stat[2 * C * tokens + at + thread] = own_z[thread];
+      const int64_t given = t0 + thread < a.M ? a.targets[t0 + thread] : a.ignore;
+      if (target_of(thread) < 0 && given != a.ignore && rank == 0) atomicCAS(a.status, 0, static_cast<int>(NF4_ERR_ARG));
+    }
+    if (kGrad) {
+      const int rows = min(kTok, a.M - t0);
+      for (int i = thread; i < rows * (a.D / 4); i += kThreads)
+        reinterpret_cast<float4*>(a.part_acc + at * a.D)[i] = reinterpret_cast<const float4*>(sums)[i];
+    }
+    return;
+  }
   if (C > 1) tc::cluster_sync();
   else __syncthreads();
 
@@ -389,41 +430,120 @@ __global__ void __launch_bounds__(kThreads, kNt == 8 ? 2 : 1) lm_small(const Sma
   if (C > 1) tc::cluster_sync();          // no CTA leaves while another reads its sums
 }
 
-constexpr int kSmemMax = 220 * 1024;
+// A token's parts joined, and 128 of its features: 8 warps down the parts, then their sums in order.
+template <bool F16>
+__global__ void __launch_bounds__(kThreads) lm_small_finish(const SmallArgs a) {
+  __shared__ float red[kWarps], factor[kPartsMax];
+  __shared__ float4 sums[kWarps][32];
+  pdl_allow_next();
+  pdl_wait();
+  const int t = blockIdx.x, thread = threadIdx.x, warp = thread >> 5, lane = thread & 31, P = a.cluster;
+  const int64_t tokens = (static_cast<int64_t>(a.M) + kTok - 1) / kTok * kTok;
+  const float *max_of = a.part_stat + t, *sum_of = max_of + P * tokens, *z_of = sum_of + P * tokens;
+  const int64_t given = a.targets[t];
+  const bool live = given >= 0 && given < a.V && given != a.ignore;
+  auto all = [&](float v, auto join) {       // over the CTA; every thread gets it
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = join(v, __shfl_xor_sync(0xffffffffu, v, o));
+    __syncthreads();
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int q = 1; q < kWarps; ++q) v = join(v, red[q]);
+    return v;
+  };
+  auto larger = [](float p, float q) { return fmaxf(p, q); };
+  auto plus = [](float p, float q) { return p + q; };
+  float m = -INFINITY, sum = 0.0f, z = 0.0f;     // (kPartsMax == kThreads: a part a thread)
+  if (thread < P) m = max_of[thread * tokens], sum = sum_of[thread * tokens], z = z_of[thread * tokens];
+  z = all(z, plus);
+  const float ref = fmaxf(z * kLog2e, all(m, larger));
+  const float f = m == ref ? 1.0f : m == -INFINITY ? 0.0f : exp2f(m - ref);
+  factor[thread] = f;
+  const float others = all(sum * f, plus);
+  const float d = fmaf(z, kLog2e, -ref), own = exp2f(d), total = others + own;     // as in lm_finish
+  if (thread == 0 && blockIdx.y == 0) {
+    const float l = d > -28.0f ? log1pf(others / own) : fmaf(-kLn2, d, logf(total));
+    a.loss[t] = live ? l : 0.0f;
+    if (a.lse != nullptr) a.lse[t] = live ? z + l : 0.0f;
+  }
+  if (a.dx == nullptr) return;
+  const int k = blockIdx.y * 128 + 4 * lane;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (k < a.D && live) {
+#pragma unroll 8
+    for (int q = warp; q < P; q += kWarps) {
+      const float4 u = *reinterpret_cast<const float4*>(a.part_acc + (q * tokens + t) * a.D + k);
+      const float w = factor[q];
+      s.x = fmaf(u.x, w, s.x), s.y = fmaf(u.y, w, s.y), s.z = fmaf(u.z, w, s.z), s.w = fmaf(u.w, w, s.w);
+    }
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || k >= a.D) return;
+#pragma unroll
+  for (int q = 1; q < kWarps; ++q) {
+    const float4 u = sums[q][lane];
+    s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
+  }
+  uint2 o = make_uint2(0, 0);
+  if (live) {
+    const float g = a.gscale == nullptr ? 1.0f : a.gscale[a.gscale_per_row ? t : 0];
+    const float p = g / total, r = g * (others / total);
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.W) + 2 * (given * a.D + k));
+    const float2 w0 = unpack16<F16>(w.x), w1 = unpack16<F16>(w.y);
+    o.x = pack16<F16>(p * s.x - r * w0.x, p * s.y - r * w0.y);
+    o.y = pack16<F16>(p * s.z - r * w1.x, p * s.w - r * w1.y);
+  }
+  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.dx) + 2 * (static_cast<int64_t>(t) * a.D + k)) = o;
+}
+
+constexpr int kSmemMax = 212 * 1024;
 
 int stages_of(int D, int split) {
   int s = kStagesMax;
   while (s > 2 && small_smem(D, split, s) > kSmemMax) --s;
   return s;
 }
-int split_of(int D) { return D <= kWarpD ? 1 : D <= 2 * kWarpD ? 2 : 4; }
+int split_of(int D) { return D <= kWarpD ? 1 : D <= 2 * kWarpD ? 2 : D <= 4 * kWarpD ? 4 : 8; }
 template <bool F16>
 auto kernel_of(int D, bool grad) {
   if (!grad) return lm_small<F16, 0, 1>;
   return D <= 64 ? lm_small<F16, 8, 1> : D <= 128 ? lm_small<F16, 16, 1> : D <= kWarpD ? lm_small<F16, 32, 1>
-         : D <= 2 * kWarpD ? lm_small<F16, 32, 2> : lm_small<F16, 32, 4>;
+         : D <= 2 * kWarpD ? lm_small<F16, 32, 2> : D <= 4 * kWarpD ? lm_small<F16, 32, 4> : lm_small<F16, 32, 8>;
 }
 
 }  // namespace
 
-// The cluster with the least estimated time in microseconds, if that is less than the launches of
-// lm_loss.cu take.  Here: a start and an end, and `steps` steps of each group one after another, as often
-// as the clusters do not fit the SMs at once (large ones leave some unused).  There: the launches'
-// latencies, the products, and the gradient's fp32 sums.  Measured with a gradient, here and there:
-// 1 x 300 x 64 6.6 and 12.4, 5 x 1038 x 144 10.1 and 13.7, 121 x 1084 x 248 12.3 and 22.6,
-// 650 x 908 x 240 14.7 and 25.4, 4096 x 1000 x 64 16 and 29, 300 x 2000 x 512 28.8 and 26.4,
-// 785 x 11051 x 600 438 and 49; without one, 1 x 300 x 64 4.9 and 9.0, 650 x 908 x 240 10.5 and 10.3.
+// Floats in front of the parts' sums.
+static size_t lm_small_stats(int64_t M, const LmSmallPlan& plan) {
+  return 3 * static_cast<size_t>(plan.cluster) * ((M + kTok - 1) / kTok * kTok);
+}
+size_t lm_small_ws_bytes(int64_t M, int64_t D, const LmSmallPlan& plan) {
+  return !plan.parts ? 0 : sizeof(float) * (lm_small_stats(M, plan) + static_cast<size_t>(plan.cluster) * ((M + kTok - 1) / kTok * kTok) * D);
+}
+
+// The form with the least estimated time in microseconds, if that is less than the launches of
+// lm_loss.cu take.  Here: a start and an end, and the steps of each group one after another, for clusters as
+// often as they do not fit the SMs at once (large ones leave some unused).  There: the launches'
+// latencies, the products or W's bytes, and the gradient's fp32 sums.  Measured with a gradient, here and
+// there, a cluster: 1 x 300 x 64 6.6 and 12.4, 5 x 1038 x 144 10.0 and 13.7, 121 x 1084 x 248 12.3 and
+// 22.6, 650 x 908 x 240 14.7 and 25.4, 4096 x 1000 x 64 16 and 29, 300 x 2000 x 512 28.8 and 26.4;
+// parts: 2 x 48757 x 1616 61 and 98, 16 x 128256 x 1024 70 and 135, 12 x 100000 x 128 17.7 and 50.7,
+// 16 x 8000 x 512 13.6 and 24.9, 37 x 13667 x 1696 52 and 37.5, 100 x 20000 x 576 68 and 35.  Without a
+// gradient, a cluster: 1 x 300 x 64 4.9 and 9.0, 650 x 908 x 240 10.5 and 10.3.
 LmSmallPlan lm_small_plan(int64_t M, int64_t V, int64_t D, bool grad) {
-  LmSmallPlan best{0};
+  LmSmallPlan best{0, false};
   if (D > (grad ? kSmallMaxD : kWarpD) || M > (1 << 16) || V > (1 << 20)) return best;
   if (wait_test_armed()) return best;        // nothing here waits long enough to give up
   const double m = static_cast<double>(M), v = static_cast<double>(V), d = static_cast<double>(D);
-  double there = grad ? (M <= kLmStreamMaxM ? 12.0 + 1.2e-6 * v * d : 20.0 + 4.0 * m * v * d / 0.8e9 + 3.3e-6 * m * d)
+  double there = grad ? (M <= kLmStreamMaxM ? 12.0 + 1.2e-6 * v * d : 20.0 + std::max(4.0 * m * v * d / 0.8e9, 0.88e-6 * v * d) + 3.3e-6 * m * d)
                       : (M <= kLmStreamMaxM ? 8.2 + 0.4e-6 * v * d : 8.2 + 0.0013 * m + 2.0 * m * v * d / 1.2e9);
   there *= 0.95;
   const int split = grad ? split_of(static_cast<int>(D)) : 1, groups = kWarps / split;
   const double ends = grad ? 6.0 + 0.0115 * d : 4.0 + 0.006 * d;
-  const double step = !grad ? 0.35 + 0.0043 * d : split == 1 ? 0.35 + 0.0051 * d : 1.0 + 0.00205 * d;
+  const double step = !grad ? 0.35 + 0.0043 * d : split == 1 ? 0.35 + 0.0051 * d : 1.9;
   const int64_t steps = (V + kRows - 1) / kRows, tiles = (M + kTok - 1) / kTok;
   const int sms = std::max(1, device_sm_count()), per_sm = D <= 64 ? 2 : 1;
   for (int c = 1; c <= kClusterMax && c <= steps; c *= 2) {
@@ -433,17 +553,24 @@ LmSmallPlan lm_small_plan(int64_t M, int64_t V, int64_t D, bool grad) {
     const double t = static_cast<double>(rounds) * (ends + crowd * step * static_cast<double>(each)) + (c > 1 ? 0.5 : 0.0);
     if (t < there) there = t, best.cluster = c;
   }
+  if (grad && tiles * kClusterMax < sms) {
+    const int64_t parts = std::min<int64_t>({sms / tiles, kPartsMax, (steps + groups - 1) / groups});
+    const int64_t each = ((steps + parts - 1) / parts + groups - 1) / groups;
+    const double t = 6.5 + 0.0085 * d + static_cast<double>(each) * (split == 1 ? 0.35 + 0.0105 * d : split == 2 ? 2.6 : 1.9);
+    if (t < there) there = t, best.cluster = static_cast<int>(parts), best.parts = true;
+  }
   return best;
 }
 
-cudaError_t launch_lm_small(const LmLossArgs& a, const LmSmallPlan& plan, const void* W, int* status, cudaStream_t st) {
+cudaError_t launch_lm_small(const LmLossArgs& a, const LmSmallPlan& plan, const void* W, void* ws, int* status,
+                            cudaStream_t st) {
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
   std::call_once(once, [] {
     auto allow = [](auto* f) {
       if (err == cudaSuccess) err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     };
-    for (const int D : {64, 128, 256, 512, 1024}) allow(kernel_of<false>(D, true)), allow(kernel_of<true>(D, true));
+    for (const int D : {64, 128, 256, 512, 1024, 2048}) allow(kernel_of<false>(D, true)), allow(kernel_of<true>(D, true));
     allow(kernel_of<false>(64, false)), allow(kernel_of<true>(64, false));
   });
   if (err != cudaSuccess) return err;
@@ -466,11 +593,20 @@ cudaError_t launch_lm_small(const LmLossArgs& a, const LmSmallPlan& plan, const 
   s.lse = a.lse;
   s.dx = a.dx;
   s.status = status;
+  if (plan.parts) {
+    s.part_stat = static_cast<float*>(ws);
+    s.part_acc = s.part_stat + lm_small_stats(a.M, plan);
+  }
   const bool grad = a.dx != nullptr;
   note_launch();
-  return launch_pdl(a.f16 ? kernel_of<true>(D, grad) : kernel_of<false>(D, grad),
-                    dim3(static_cast<unsigned>((a.M + kTok - 1) / kTok * plan.cluster)), dim3(kThreads),
-                    static_cast<size_t>(small_smem(D, split, s.stages)), st, static_cast<unsigned>(plan.cluster), s);
+  const cudaError_t e =
+      launch_pdl(a.f16 ? kernel_of<true>(D, grad) : kernel_of<false>(D, grad),
+                 dim3(static_cast<unsigned>((a.M + kTok - 1) / kTok * plan.cluster)), dim3(kThreads),
+                 static_cast<size_t>(small_smem(D, split, s.stages)), st, plan.parts ? 1u : static_cast<unsigned>(plan.cluster), s);
+  if (e != cudaSuccess || !plan.parts) return e;
+  note_launch();
+  return launch_pdl(a.f16 ? lm_small_finish<true> : lm_small_finish<false>,
+                    dim3(static_cast<unsigned>(a.M), static_cast<unsigned>(grad ? (D + 127) / 128 : 1)), dim3(kThreads), 0, st, 1, s);
 }
 
 }  // namespace qnf4

@@ -413,10 +413,13 @@ def test_loss(lib, dtype, M, V, D):
 LOSS_EDGES = [(15, 15, 64), (16, 16, 72), (17, 17, 88), (33, 1500, 120), (1, 31, 128), (40, 129, 136), (100, 900, 256),
               (20, 500, 264), (50, 300, 512), (6, 170, 520), (3, 100, 1024), (700, 600, 64), (3000, 90, 80),
               (300, 30000, 136), (7, 60000, 72), (100, 20000, 576), (1, 40000, 256), (500, 9000, 1024)]
+# few tokens over a vocabulary that every SM takes a part of
+LOSS_PARTS = [(2, 9000, 1616), (16, 9001, 512), (17, 5000, 256), (33, 7001, 136), (9, 3000, 1032), (1, 9000, 2048),
+              (12, 20000, 64), (3, 700, 216)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("M,V,D", LOSS_EDGES)
+@pytest.mark.parametrize("M,V,D", LOSS_EDGES + LOSS_PARTS)
 def test_loss_in_one_launch_or_several(lib, dtype, M, V, D):
     x, W, t = _loss_case(M, V, D, dtype, 7)
     tt = torch.from_numpy(t).to(DEV)
