@@ -4,8 +4,9 @@
 // registers and stay in flight across the reductions, which is what keeps HBM busy.
 //
 // A bulk copy moves whole 16-byte pieces.  Rows that start or end inside one are copied with the
-// pieces around them and read in pairs (train_ops.cuh) from where they start in the stage.  A worker's rows are an
-// even number apart, so they all start at the same parity and a thread's columns are the same for all.
+// pieces around them and read in pairs (train_ops.cuh) from where they start in the stage.  A
+// worker's rows are an even number apart, so they all start at the same parity and a thread's
+// columns are the same for all.
 #pragma once
 
 #include "tc_ptx.cuh"
